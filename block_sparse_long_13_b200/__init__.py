@@ -29,6 +29,8 @@ EXPORTS = (
     "msa_set_wait_limit_ns", "msa_debug_wait_timeout", "msa_status_string", "msa_last_error",
     "msa_version", "msa_attn_decode_noalloc", "msa_index_topk", "msa_set_timing_events",
     "msa_qknorm_rope_insert", "msa_merge_partials", "msa_index_scores_fp8",
+    "msa_attn_decode_fp8", "msa_attn_prefill_fp8", "msa_decode_fp8_workspace_bytes", "msa_prefill_fp8_workspace_bytes",
+    "msa_qknorm_rope_insert_fp8", "msa_advance_batch",
 )
 
 MSA_OK, MSA_ERR_INVALID_ARG, MSA_ERR_UNSUPPORTED, MSA_ERR_CUDA, MSA_ERR_TIMEOUT, MSA_ERR_DEVICE_BOUNDS = range(6)
@@ -80,6 +82,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "msa_merge_partials": [ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, P, P, P, P, P],
         "msa_prefill_workspace_bytes": [cfgp, batp],
         "msa_decode_workspace_bytes": [cfgp, batp],
+        "msa_attn_decode_fp8": [cfgp, batp, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P],
+        "msa_attn_prefill_fp8": [cfgp, batp, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P],
+        "msa_decode_fp8_workspace_bytes": [cfgp, batp],
+        "msa_prefill_fp8_workspace_bytes": [cfgp, batp],
+        "msa_qknorm_rope_insert_fp8": [cfgp, batp, P, P, P, P, P, P, P, P, P, P, ctypes.c_int32, ctypes.c_float,
+                                       ctypes.c_float, P],
+        "msa_advance_batch": [ctypes.c_int32] * 4 + [P] * 9 + [ctypes.c_int32, P],
         "msa_get_device_status": [P],
         "msa_set_wait_limit_ns": [ctypes.c_uint64],
         "msa_debug_wait_timeout": [P],
@@ -91,8 +100,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = ctypes.c_int
-    lib.msa_prefill_workspace_bytes.restype = ctypes.c_size_t
-    lib.msa_decode_workspace_bytes.restype = ctypes.c_size_t
+    for name in ("msa_prefill_workspace_bytes", "msa_decode_workspace_bytes", "msa_prefill_fp8_workspace_bytes",
+                 "msa_decode_fp8_workspace_bytes"):
+        getattr(lib, name).restype = ctypes.c_size_t
     lib.msa_status_string.restype = ctypes.c_char_p
     lib.msa_last_error.restype = ctypes.c_char_p
     _lib_handle = lib
@@ -267,6 +277,96 @@ def qknorm_rope_insert(cfg: Config, batch: Batch, q, k_new, v_new, q_norm_w, k_n
                                       _need(k_norm_w, torch.bfloat16, "k_norm_w"),
                                       _need(k_cache, torch.bfloat16, "k_cache"), _need(v_cache, torch.bfloat16, "v_cache"),
                                       int(rotary_dim), float(rope_theta), float(eps), _stream(stream)))
+
+
+def _pointers(*arrays):
+    """Device pointers of (tensor, dtype, shape, name) arguments; a None tensor is 0.  The shapes are checked first,
+    then what _need checks, and that every tensor is on the current device."""
+    for t, _, shape, what in arrays:
+        if t is not None and t.shape != shape:
+            raise MsaError(MSA_ERR_INVALID_ARG, f"{what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    out = [_need(t, dtype, what) for t, dtype, _, what in arrays]
+    here = torch.cuda.current_device()
+    for t, _, _, what in arrays:
+        if t is not None and t.get_device() != here:
+            raise MsaError(MSA_ERR_INVALID_ARG, f"{what} is on device {t.get_device()}, but device {here} is current")
+    return out
+
+
+def _fp8_cache(cfg: Config, batch: Batch, k_cache, v_cache, k_scale, v_scale):
+    tiles = (batch.num_pages, cfg.num_kv_heads)
+    cache = tiles + (cfg.block_size, cfg.head_dim)
+    return ((k_cache, torch.uint8, cache, "k_cache_e4m3"), (v_cache, torch.uint8, cache, "v_cache_e4m3"),
+            (k_scale, torch.float32, tiles, "k_scale"), (v_scale, torch.float32, tiles, "v_scale"))
+
+
+def prefill_fp8_workspace_bytes(cfg: Config, batch: Batch) -> int:
+    return int(load_library().msa_prefill_fp8_workspace_bytes(ctypes.byref(cfg._c()),
+                                                              ctypes.byref(batch._c(host_only=True))))
+
+
+def decode_fp8_workspace_bytes(cfg: Config, batch: Batch) -> int:
+    return int(load_library().msa_decode_fp8_workspace_bytes(ctypes.byref(cfg._c()),
+                                                             ctypes.byref(batch._c(host_only=True))))
+
+
+def _attn_fp8(fn, cfg, batch, q, k_cache, v_cache, k_scale, v_scale, block_idx, out, lse, workspace, stream):
+    rows = (batch.total_q, cfg.num_q_heads)
+    bf16, heads = torch.bfloat16, rows + (cfg.head_dim,)
+    nbytes = workspace.numel() if workspace is not None else 0
+    ptrs = _pointers((q, bf16, heads, "q"), *_fp8_cache(cfg, batch, k_cache, v_cache, k_scale, v_scale),
+                     (block_idx, torch.int32, (batch.total_q, cfg.num_kv_heads, cfg.topk), "block_idx"),
+                     (out, bf16, heads, "out"), (lse, torch.float32, rows, "lse"),
+                     (workspace, torch.uint8, (nbytes,), "workspace"))
+    _check(fn(ctypes.byref(cfg._c()), ctypes.byref(batch._c()), *ptrs, nbytes, _stream(stream)))
+
+
+def attn_decode_fp8(cfg: Config, batch: Batch, q, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale, block_idx, out, lse=None,
+                    workspace=None, stream=None) -> None:
+    """attn_decode over a cache of e4m3 codes (uint8 [num_pages][num_kv_heads][128][128]) with a scale for each
+    (page, KV head) (fp32 [num_pages][num_kv_heads]); value = code * scale.  For few queries per sequence."""
+    _attn_fp8(load_library().msa_attn_decode_fp8, cfg, batch, q, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale, block_idx,
+              out, lse, workspace, stream)
+
+
+def attn_prefill_fp8(cfg: Config, batch: Batch, q, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale, block_idx, out, lse=None,
+                     workspace=None, stream=None) -> None:
+    """attn_decode_fp8's results, organised for many queries per sequence."""
+    _attn_fp8(load_library().msa_attn_prefill_fp8, cfg, batch, q, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale, block_idx,
+              out, lse, workspace, stream)
+
+
+def qknorm_rope_insert_fp8(cfg: Config, batch: Batch, q, k_new, v_new, q_norm_w, k_norm_w, q_out, k_cache_e4m3,
+                           v_cache_e4m3, k_scale, v_scale, rotary_dim: int = 64, rope_theta: float = 10000.0,
+                           eps: float = 1e-6, stream=None) -> None:
+    """qknorm_rope_insert into an 8-bit cache (see include/msa.h): the queries go to q_out (q itself or another
+    buffer), the new rows become codes, and the scales of their pages follow."""
+    bf16, heads, new = torch.bfloat16, (batch.total_q, cfg.num_q_heads, cfg.head_dim), (batch.total_q, cfg.num_kv_heads, cfg.head_dim)
+    ptrs = _pointers((q, bf16, heads, "q"), (k_new, bf16, new, "k_new"), (v_new, bf16, new, "v_new"),
+                     (q_norm_w, bf16, new[2:], "q_norm_w"), (k_norm_w, bf16, new[2:], "k_norm_w"), (q_out, bf16, heads, "q_out"),
+                     *_fp8_cache(cfg, batch, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale))
+    _check(load_library().msa_qknorm_rope_insert_fp8(ctypes.byref(cfg._c()), ctypes.byref(batch._c()), *ptrs, int(rotary_dim),
+                                                     float(rope_theta), float(eps), _stream(stream)))
+
+
+def advance_batch(delta, ctx_len, page_table, free_ring, pool, ctx_len_out, pool_out, q_start, slot_map=None,
+                  block_size: int = 128, stream=None) -> None:
+    """The index arrays of a step from the requests' signed token counts (see include/msa.h): pages are taken from and
+    given back to the ring, and ctx_len_out, q_start and page_table then serve as a Batch.  ctx_len_out may be ctx_len
+    and pool_out may be pool.  All tensors int32; nothing is read back to the host: pool_out[2] says on the device how
+    many pages the step lacked (0: done, -1: arguments that do not fit)."""
+    if page_table.dim() != 2:
+        raise MsaError(MSA_ERR_INVALID_ARG, "page_table must be [num_seqs][max_blocks_per_seq]")
+    n, width = page_table.shape
+    pages, rows = free_ring.numel(), slot_map.numel() if slot_map is not None else 0
+    i32 = torch.int32
+    ptrs = _pointers((delta, i32, (n,), "delta"), (ctx_len, i32, (n,), "ctx_len"), (page_table, i32, (n, width), "page_table"),
+                     (free_ring, i32, (pages,), "free_ring"), (pool, i32, (4,), "pool"), (ctx_len_out, i32, (n,), "ctx_len_out"),
+                     (pool_out, i32, (4,), "pool_out"), (q_start, i32, (n + 1,), "q_start"),
+                     (slot_map, i32, (rows,), "slot_map"))
+    if rows == 0:
+        ptrs[8] = 0                    # an empty slot map is none
+    _check(load_library().msa_advance_batch(n, width, pages, int(block_size), *ptrs, rows, _stream(stream)))
 
 
 def merge_partials(outs, lses, out, lse=None, stream=None) -> None:

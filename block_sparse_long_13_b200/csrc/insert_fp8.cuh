@@ -1,0 +1,321 @@
+// msa_qknorm_rope_insert_fp8: per-head QK RMSNorm, partial rotary embedding and the insert of the new K and
+// V rows into a paged cache of e4m3 codes with one fp32 scale for each (page, KV head).
+//
+//   q_out[t][h]  = rope(rmsnorm(q[t][h]) * q_norm_w)                              (bf16)
+//   y_k[t][g]    = rope(rmsnorm(k_new[t][g]) * k_norm_w),  y_v[t][g] = v_new[t][g]   (fp32, never rounded to bf16)
+// and for every (page, g) that the call's rows touch, K and V alike, with a = the largest finite |y| among
+// the page's new rows and old = the scale before the call:
+//   scale = fit(a)                     if the page begins with one of the call's rows (slot 0 is written)
+//         = old                        otherwise, if a <= 448 old
+//         = fit(a), and the codes of the page's older rows become e4m3(code * old / scale)  otherwise
+//   code[slot] = e4m3(saturate(y / scale)),    fit(a) = the least power of two with 448 fit(a) >= a.
+// Rows behind the page's last new row are left as they were.
+//
+// Two kernels.  kv_insert_fp8_kernel: a CTA owns one (page, head) piece, i.e. up to 128 consecutive rows of one
+// sequence inside one block, because the scale needs all of them before any code can be written.  Half a warp
+// takes a row's head; the rows stay in registers between the maximum and the rounding, so K and V are read
+// once.  The pieces are the first block of each sequence (CTA = sequence) and the blocks that begin inside
+// the call's rows (CTA = window of 128 rows, which holds one such block for each sequence that crosses a
+// block border in it): num_seqs + total_q / 128 CTAs a head, no search by the host.
+// q_norm_rope_kernel: one CTA a row, in and out by bulk copies.
+//
+// Angles: p * theta^(-2i/r) is taken in turns, in double, from a table that the host fills (theta^(-2i/r) / 2 pi):
+// the fraction of a turn is exact to 2^-31 at positions up to 2^22, and cospi / sinpi of it in fp32 lose
+// nothing further, where a double sincos would cost some hundred double instructions a pair.
+#pragma once
+#include "e4m3.cuh"
+#include "qk_rope_insert.cuh"
+
+namespace msa {
+
+constexpr int KVI_THREADS = 256;                       // 16 half-warps, a row's head each
+constexpr int KVI_ITERS = 128 / (KVI_THREADS / 16);    // rows of a full page per half-warp
+
+struct RopeTable { double turns[QKR_D / 2]; };         // theta^(-2i/r) / (2 pi), i < rotary_dim / 2
+
+struct KvInsertArgs {
+  const __nv_bfloat16* k_new;    // [total_q][Hkv][128]
+  const __nv_bfloat16* v_new;
+  const __nv_bfloat16* k_w;      // [128]
+  uint8_t* k_cache;              // [pages][Hkv][128][128] codes
+  uint8_t* v_cache;
+  float* k_scale;                // [pages][Hkv]
+  float* v_scale;
+  const int32_t* q_start;
+  const int32_t* ctx_len;
+  const int32_t* page_table;
+  int num_seqs, total_q, Hkv, max_blocks, num_pages, rotary_dim;
+  float eps;
+};
+
+// cos and sin of the angle of pair i at position p
+__device__ __forceinline__ void rope_angle(double turns, int p, float& cs, float& sn) {
+  const double a = static_cast<double>(p) * turns;
+  const float f = static_cast<float>(a - rint(a)) * 2.f;   // half turns in [-1, 1]
+  sincospif(f, &sn, &cs);
+}
+
+__device__ __forceinline__ float finite_abs(float x) {   // |x|, 0 for infinities and NaN
+  const float a = fabsf(x);
+  return a < INFINITY ? a : 0.f;
+}
+
+// Codes of the older rows of a page after its scale grew: e4m3(code * ratio).
+__device__ __forceinline__ void rescale_codes(uint8_t* tile, int rows, float ratio) {
+  for (int i = threadIdx.x; i < rows * 8; i += KVI_THREADS) {
+    uint4* p = reinterpret_cast<uint4*>(tile) + i;
+    uint4 w = *p;
+    uint32_t* u = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float x[4];
+      e4m3x4_value(u[j], x);
+      u[j] = e4m3x4_of(x[0] * ratio, x[1] * ratio, x[2] * ratio, x[3] * ratio);
+    }
+    *p = w;
+  }
+}
+
+// One piece: rows t0 .. t0 + n - 1 at positions p0 .. of one block, KV head g, page `page` (valid).
+__device__ __forceinline__ void kv_insert_piece(const KvInsertArgs& a, const RopeTable& tab, int t0, int p0, int n, int page,
+                                                int g, float (&s_max)[2][KVI_THREADS / 32]) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hl = lane & 15;
+  const int row0 = warp * 2 + (lane >> 4);
+  const int slot0 = p0 & 127;
+  const long tile = static_cast<long>(page) * a.Hkv + g;
+  const float k_old = a.k_scale[tile], v_old = a.v_scale[tile];
+
+  // this lane's quads of a K row: a rotation pair (qa, qa + r/8) or two pass-through quads; of a V row: 8 dims
+  const int P = a.rotary_dim >> 3;
+  const bool rot = hl < P;
+  const int qa = rot ? hl : 2 * P + 2 * (hl - P);
+  const int ca = 4 * qa, cb = 4 * (rot ? hl + P : qa + 1);
+
+  uint2 ka[KVI_ITERS], kb[KVI_ITERS];
+  uint4 vv[KVI_ITERS];
+#pragma unroll
+  for (int it = 0; it < KVI_ITERS; ++it) {
+    const int r = it * 16 + row0;
+    ka[it] = kb[it] = make_uint2(0u, 0u);
+    vv[it] = make_uint4(0u, 0u, 0u, 0u);
+    if (r < n) {
+      const long at = (static_cast<long>(t0 + r) * a.Hkv + g) * QKR_D;
+      ka[it] = __ldg(reinterpret_cast<const uint2*>(a.k_new + at + ca));
+      kb[it] = __ldg(reinterpret_cast<const uint2*>(a.k_new + at + cb));
+      vv[it] = __ldg(reinterpret_cast<const uint4*>(a.v_new + at) + hl);
+    }
+  }
+  float wa[4], wb[4];
+  load_bf16x4(a.k_w + ca, wa);
+  load_bf16x4(a.k_w + cb, wb);
+  double turns[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) turns[u] = rot ? tab.turns[ca + u] : 0.0;
+
+  float ky[KVI_ITERS][8];
+  float kmax = 0.f, vmax = 0.f;
+#pragma unroll
+  for (int it = 0; it < KVI_ITERS; ++it) {
+    if (it * 16 >= n) break;                             // uniform
+    float xa[4] = {bf16lo(ka[it].x), bf16hi(ka[it].x), bf16lo(ka[it].y), bf16hi(ka[it].y)};
+    float xb[4] = {bf16lo(kb[it].x), bf16hi(kb[it].x), bf16lo(kb[it].y), bf16hi(kb[it].y)};
+    float ss = 0.f;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) ss += xa[u] * xa[u] + xb[u] * xb[u];
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+    const float inv = rsqrtf(ss * (1.f / QKR_D) + a.eps);
+    const int p = p0 + it * 16 + row0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float ya = xa[u] * inv * wa[u], yb = xb[u] * inv * wb[u];
+      float cs = 1.f, sn = 0.f;
+      if (rot) rope_angle(turns[u], p, cs, sn);
+      ky[it][u] = rot ? ya * cs - yb * sn : ya;
+      ky[it][4 + u] = rot ? yb * cs + ya * sn : yb;
+    }
+    if (it * 16 + row0 < n) {                            // rows past the piece hold nothing
+#pragma unroll
+      for (int u = 0; u < 8; ++u) kmax = fmaxf(kmax, finite_abs(ky[it][u]));
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(&vv[it]);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) vmax = fmaxf(vmax, fmaxf(finite_abs(bf16lo(w[u])), finite_abs(bf16hi(w[u]))));
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    kmax = fmaxf(kmax, __shfl_xor_sync(0xFFFFFFFFu, kmax, o));
+    vmax = fmaxf(vmax, __shfl_xor_sync(0xFFFFFFFFu, vmax, o));
+  }
+  if (lane == 0) { s_max[0][warp] = kmax; s_max[1][warp] = vmax; }
+  __syncthreads();                                       // every thread has read the old scales
+#pragma unroll
+  for (int w = 0; w < KVI_THREADS / 32; ++w) {
+    kmax = fmaxf(kmax, s_max[0][w]);
+    vmax = fmaxf(vmax, s_max[1][w]);
+  }
+  // a scale that is not positive holds nothing: it counts as 0
+  const bool k_grown = slot0 == 0 || !(k_old > 0.f) || kmax > E4M3_MAX * k_old;
+  const bool v_grown = slot0 == 0 || !(v_old > 0.f) || vmax > E4M3_MAX * v_old;
+  const float ks = k_grown ? e4m3_block_scale(kmax) : k_old, vs = v_grown ? e4m3_block_scale(vmax) : v_old;
+  uint8_t* kt = a.k_cache + tile * (128 * QKR_D);
+  uint8_t* vt = a.v_cache + tile * (128 * QKR_D);
+#pragma unroll
+  for (int it = 0; it < KVI_ITERS; ++it) {
+    const int r = it * 16 + row0;
+    if (r >= n) break;
+    uint8_t* kr = kt + (slot0 + r) * QKR_D;
+    float z[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) z[u] = __fdiv_rn(ky[it][u], ks);
+    *reinterpret_cast<uint32_t*>(kr + ca) = e4m3x4_of(z[0], z[1], z[2], z[3]);
+    *reinterpret_cast<uint32_t*>(kr + cb) = e4m3x4_of(z[4], z[5], z[6], z[7]);
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&vv[it]);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) { z[2 * u] = __fdiv_rn(bf16lo(w[u]), vs); z[2 * u + 1] = __fdiv_rn(bf16hi(w[u]), vs); }
+    *reinterpret_cast<uint2*>(vt + (slot0 + r) * QKR_D + 8 * hl) =
+        make_uint2(e4m3x4_of(z[0], z[1], z[2], z[3]), e4m3x4_of(z[4], z[5], z[6], z[7]));
+  }
+  if (slot0 > 0 && k_grown) rescale_codes(kt, slot0, k_old > 0.f ? __fdiv_rn(k_old, ks) : 0.f);
+  if (slot0 > 0 && v_grown) rescale_codes(vt, slot0, v_old > 0.f ? __fdiv_rn(v_old, vs) : 0.f);
+  if (tid == 0) {
+    if (k_grown) a.k_scale[tile] = ks;
+    if (v_grown) a.v_scale[tile] = vs;
+  }
+}
+
+__global__ void __launch_bounds__(KVI_THREADS)
+kv_insert_fp8_kernel(const KvInsertArgs a, const __grid_constant__ RopeTable tab) {
+  __shared__ float s_max[2][KVI_THREADS / 32];
+  __shared__ int s_t[128], s_p[128], s_s[128], s_cnt[4];
+  const int g = blockIdx.x % a.Hkv, i = blockIdx.x / a.Hkv;
+  // the cache page of sequence s's block b; -1 (and flagged) if there is none
+  auto page_of = [&](int s, int b) -> int {
+    const int page = b >= 0 && b < a.max_blocks ? __ldg(a.page_table + static_cast<long>(s) * a.max_blocks + b) : -1;
+    if (page >= 0 && page < a.num_pages) return page;
+    if (threadIdx.x == 0) flag_error(MSA_DEV_BOUNDS);
+    return -1;
+  };
+  if (i < a.num_seqs) {                                  // the block that the sequence's first new row falls in
+    const int t0 = __ldg(a.q_start + i), nq = __ldg(a.q_start + i + 1) - t0, p0 = __ldg(a.ctx_len + i) - nq;
+    if (nq <= 0) return;
+    if (p0 < 0 || t0 < 0 || t0 + nq > a.total_q) {
+      if (threadIdx.x == 0) flag_error(MSA_DEV_BOUNDS);
+      return;
+    }
+    const int page = page_of(i, p0 >> 7);
+    if (page >= 0) kv_insert_piece(a, tab, t0, p0, min(nq, 128 - (p0 & 127)), page, g, s_max);
+    return;
+  }
+  // the blocks that begin at a row of this window (not their sequence's first row)
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rows = min(a.total_q, __ldg(a.q_start + a.num_seqs));
+  unsigned vote = 0;
+  int t = 0, s = 0, p = 0;
+  bool lead = false;
+  if (tid < 128) {
+    t = (i - a.num_seqs) * 128 + tid;
+    if (t < rows) {
+      s = find_seq(a.q_start, a.num_seqs, t);
+      const int end = __ldg(a.q_start + s + 1);
+      p = __ldg(a.ctx_len + s) - end + t;
+      lead = t != __ldg(a.q_start + s) && p > 0 && (p & 127) == 0;
+    }
+    vote = __ballot_sync(0xFFFFFFFFu, lead);
+    if (lane == 0) s_cnt[warp] = __popc(vote);
+  }
+  __syncthreads();
+  if (lead) {
+    int at = __popc(vote & ((1u << lane) - 1u));
+    for (int w = 0; w < warp; ++w) at += s_cnt[w];
+    s_t[at] = t; s_p[at] = p; s_s[at] = s;
+  }
+  __syncthreads();
+  const int n_lead = s_cnt[0] + s_cnt[1] + s_cnt[2] + s_cnt[3];
+  for (int j = 0; j < n_lead; ++j) {
+    const int page = page_of(s_s[j], s_p[j] >> 7);
+    if (page >= 0)
+      kv_insert_piece(a, tab, s_t[j], s_p[j], min(128, min(rows, __ldg(a.q_start + s_s[j] + 1)) - s_t[j]), page, g, s_max);
+    __syncthreads();                                     // s_max is written again
+  }
+}
+
+struct QNormRopeArgs {
+  const __nv_bfloat16* q;        // [total_q][Hq][128]
+  __nv_bfloat16* q_out;          // the same shape, q itself or disjoint
+  const __nv_bfloat16* q_w;      // [128]
+  const int32_t* q_start;
+  const int32_t* ctx_len;
+  int num_seqs, total_q, Hq, rotary_dim;
+  float eps;
+};
+
+__global__ void __launch_bounds__(QKR_THREADS)
+q_norm_rope_kernel(const QNormRopeArgs a, const __grid_constant__ RopeTable tab) {
+  extern __shared__ __align__(128) uint8_t qnr_dsmem[];
+  __nv_bfloat16* xs = reinterpret_cast<__nv_bfloat16*>(qnr_dsmem);   // [Hq][128]
+  __shared__ float s_cos[QKR_D / 2], s_sin[QKR_D / 2];
+  __shared__ __align__(16) float s_w[QKR_D];
+  __shared__ uint64_t s_bar;
+  __shared__ volatile int s_abort;
+  const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t bytes = static_cast<uint32_t>(a.Hq) * QKR_D * 2;
+  if (tid == 0) {
+    s_abort = 0;
+    mbar_init(&s_bar, 1);
+    fence_mbar_init();
+    mbar_arrive_expect_tx(&s_bar, bytes);
+    bulk_load(xs, a.q + static_cast<long>(t) * a.Hq * QKR_D, bytes, &s_bar);
+  }
+  const int s = find_seq(a.q_start, a.num_seqs, t);
+  const int end = __ldg(a.q_start + s + 1);
+  const bool padded = t >= end;                          // a row behind the last sequence: left as it was
+  const int p = __ldg(a.ctx_len + s) - end + t;
+  if (tid < a.rotary_dim / 2) rope_angle(tab.turns[tid], p, s_cos[tid], s_sin[tid]);
+  if (tid < QKR_D) s_w[tid] = __bfloat162float(a.q_w[tid]);
+  const int hl = lane & 15, P = a.rotary_dim >> 3;
+  const bool rot = hl < P;
+  const int qa = rot ? hl : 2 * P + 2 * (hl - P);
+  const int ca = 4 * qa, cb = 4 * (rot ? hl + P : qa + 1);
+  __syncthreads();
+  if (tid == 0 && !mbar_wait(&s_bar, 0, &s_abort)) mbar_wait_drain(&s_bar, 0);
+  __syncthreads();
+  if (s_abort || padded) return;
+  float cs[4], sn[4], wa[4], wb[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    cs[u] = rot ? s_cos[ca + u] : 1.f;
+    sn[u] = rot ? s_sin[ca + u] : 0.f;
+    wa[u] = s_w[ca + u];
+    wb[u] = s_w[cb + u];
+  }
+  for (int j = 2 * warp + (lane >> 4); j < a.Hq; j += QKR_THREADS / 16) {   // Hq is a multiple of 16: uniform
+    __nv_bfloat16* row = xs + j * QKR_D;
+    float xa[4], xb[4], oa[4], ob[4];
+    load_bf16x4(row + ca, xa);
+    load_bf16x4(row + cb, xb);
+    float ss = 0.f;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) ss += xa[u] * xa[u] + xb[u] * xb[u];
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+    const float inv = rsqrtf(ss * (1.f / QKR_D) + a.eps);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float ya = xa[u] * inv * wa[u], yb = xb[u] * inv * wb[u];
+      oa[u] = rot ? ya * cs[u] - yb * sn[u] : ya;
+      ob[u] = rot ? yb * cs[u] + ya * sn[u] : yb;
+    }
+    store_bf16x4(row + ca, oa);
+    store_bf16x4(row + cb, ob);
+  }
+  fence_proxy_async_smem();
+  __syncthreads();
+  if (tid == 0) {
+    bulk_store(a.q_out + static_cast<long>(t) * a.Hq * QKR_D, xs, bytes);
+    bulk_commit();
+    bulk_wait_all();
+  }
+}
+
+}  // namespace msa

@@ -11,12 +11,15 @@
 #include <mutex>
 
 #include "../../include/msa.h"
+#include "advance_batch.cuh"
 #include "attn_decode.cuh"
+#include "attn_fp8.cuh"
 #include "attn_prefill.cuh"
 #include "common.cuh"
 #include "index_decode.cuh"
 #include "index_decode_tc.cuh"
 #include "index_prefill.cuh"
+#include "insert_fp8.cuh"
 #include "merge_partials.cuh"
 #include "qk_rope_insert.cuh"
 #include "topk.cuh"
@@ -54,6 +57,7 @@ msa_status_t fail(msa_status_t st, const char* fmt, ...) {
   } while (0)
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 float softmax_scale(const msa_config_t* c) {
   return c->softmax_scale > 0.f ? c->softmax_scale : 1.0f / std::sqrt(static_cast<float>(c->head_dim));
@@ -765,3 +769,196 @@ extern "C" msa_status_t msa_attn_decode_noalloc(const msa_config_t* cfg, const m
                          stream);
 }
 
+
+// ---------------------------------------------------------------- the 8-bit K/V cache
+namespace {
+
+// What both attention calls over the 8-bit cache check.
+msa_status_t check_attn_fp8(const msa_config_t* cfg, const msa_batch_t* batch, const void* q, const void* k, const void* v,
+                            const float* k_scale, const float* v_scale, const int32_t* block_idx, const void* out,
+                            const float* lse, const void* workspace, size_t have, size_t need) {
+  msa_status_t st;
+  if ((st = check_config(cfg)) != MSA_OK) return st;
+  if ((st = check_batch(batch)) != MSA_OK) return st;
+  CHECK_ARG(q && k && v && k_scale && v_scale && block_idx && out,
+            "q, the caches, their scales, block_idx and out must not be NULL");
+  CHECK_ARG(aligned16(q) && aligned16(k) && aligned16(v) && aligned16(out) && aligned16(workspace),
+            "q, caches, out and workspace must be 16-byte aligned");
+  CHECK_ARG(aligned4(k_scale) && aligned4(v_scale) && aligned4(block_idx) && aligned4(lse),
+            "scales, block_idx and lse must be 4-byte aligned");
+  CHECK_ARG(workspace != nullptr && have >= need, "workspace too small: %zu bytes needed", need);
+  CHECK_SUP(static_cast<int64_t>(batch->num_pages) * cfg->num_kv_heads * 128 < (1LL << 31), "the cache has too many rows");
+  CHECK_SUP(static_cast<int64_t>(batch->total_q) * cfg->num_kv_heads * cfg->topk < (1LL << 31),
+            "too many (row, group, slot) entries");
+  return MSA_OK;
+}
+
+msa_status_t run_attn_fp8(const msa_config_t* cfg, const msa_batch_t* batch, const void* q, const void* k, const void* v,
+                          const float* k_scale, const float* v_scale, const int32_t* block_idx, void* out, float* lse,
+                          cudaStream_t stream) {
+  msa::AttnFp8Args a{};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k_cache = static_cast<const uint8_t*>(k);
+  a.v_cache = static_cast<const uint8_t*>(v);
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.block_idx = block_idx;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  a.q_start = batch->q_start;
+  a.ctx_len = batch->ctx_len;
+  a.page_table = batch->page_table;
+  a.num_seqs = batch->num_seqs;
+  a.total_q = batch->total_q;
+  a.Hq = cfg->num_q_heads;
+  a.Hkv = cfg->num_kv_heads;
+  a.topk = cfg->topk;
+  a.max_blocks = batch->max_blocks_per_seq;
+  a.num_pages = batch->num_pages;
+  a.scale_log2 = softmax_scale(cfg) * 1.4426950408889634f;
+  msa::attn_fp8_plain_kernel<<<static_cast<unsigned>(batch->total_q) * cfg->num_kv_heads, 128, 0, stream>>>(a);
+  return launched();
+}
+
+// theta^(-2i/r) / (2 pi) for the rotation pairs
+msa::RopeTable rope_table(int rotary_dim, float theta) {
+  msa::RopeTable t{};
+  const double l2 = std::log2(static_cast<double>(theta));
+  for (int i = 0; i < rotary_dim / 2; ++i) t.turns[i] = std::exp2(-(2.0 * i / rotary_dim) * l2) * 0.15915494309189533577;
+  return t;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t msa_decode_fp8_workspace_bytes(const msa_config_t* cfg, const msa_batch_t* batch) {
+  if (check_config(cfg) != MSA_OK || check_batch(batch) != MSA_OK) return 0;
+  return 256;
+}
+
+size_t msa_prefill_fp8_workspace_bytes(const msa_config_t* cfg, const msa_batch_t* batch) {
+  if (check_config(cfg) != MSA_OK || check_batch(batch) != MSA_OK) return 0;
+  return 256;
+}
+
+msa_status_t msa_attn_decode_fp8(const msa_config_t* cfg, const msa_batch_t* batch, const void* q,
+                                 const void* k_cache_e4m3, const void* v_cache_e4m3, const float* k_scale,
+                                 const float* v_scale, const int32_t* block_idx, void* out, float* lse, void* workspace,
+                                 size_t workspace_bytes, cudaStream_t stream) {
+  msa_status_t st = check_attn_fp8(cfg, batch, q, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale, block_idx, out, lse,
+                                   workspace, workspace_bytes, msa_decode_fp8_workspace_bytes(cfg, batch));
+  if (st != MSA_OK || batch->total_q == 0) return st;
+  return run_attn_fp8(cfg, batch, q, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale, block_idx, out, lse, stream);
+}
+
+msa_status_t msa_attn_prefill_fp8(const msa_config_t* cfg, const msa_batch_t* batch, const void* q,
+                                  const void* k_cache_e4m3, const void* v_cache_e4m3, const float* k_scale,
+                                  const float* v_scale, const int32_t* block_idx, void* out, float* lse, void* workspace,
+                                  size_t workspace_bytes, cudaStream_t stream) {
+  msa_status_t st = check_attn_fp8(cfg, batch, q, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale, block_idx, out, lse,
+                                   workspace, workspace_bytes, msa_prefill_fp8_workspace_bytes(cfg, batch));
+  if (st != MSA_OK || batch->total_q == 0) return st;
+  return run_attn_fp8(cfg, batch, q, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale, block_idx, out, lse, stream);
+}
+
+msa_status_t msa_qknorm_rope_insert_fp8(const msa_config_t* cfg, const msa_batch_t* batch, const void* q,
+                                        const void* k_new, const void* v_new, const void* q_norm_w,
+                                        const void* k_norm_w, void* q_out, void* k_cache_e4m3, void* v_cache_e4m3,
+                                        float* k_scale, float* v_scale, int32_t rotary_dim, float rope_theta, float eps,
+                                        cudaStream_t stream) {
+  msa_status_t st;
+  if ((st = check_config(cfg)) != MSA_OK) return st;
+  if ((st = check_batch(batch)) != MSA_OK) return st;
+  CHECK_ARG(q && k_new && v_new && q_norm_w && k_norm_w && q_out && k_cache_e4m3 && v_cache_e4m3 && k_scale && v_scale,
+            "q, k_new, v_new, the norm weights, q_out, the caches and their scales must not be NULL");
+  CHECK_ARG(aligned16(q) && aligned16(k_new) && aligned16(v_new) && aligned16(q_norm_w) && aligned16(k_norm_w) &&
+                aligned16(q_out) && aligned16(k_cache_e4m3) && aligned16(v_cache_e4m3),
+            "q, k_new, v_new, norm weights, q_out and caches must be 16-byte aligned");
+  CHECK_ARG(aligned4(k_scale) && aligned4(v_scale), "the scales must be 4-byte aligned");
+  CHECK_ARG(rotary_dim > 0 && rotary_dim % 8 == 0 && rotary_dim <= cfg->head_dim,
+            "rotary_dim must be a positive multiple of 8, at most head_dim");
+  CHECK_ARG(std::isfinite(rope_theta) && rope_theta > 0.f, "rope_theta must be positive and finite");
+  CHECK_ARG(std::isfinite(eps) && eps >= 0.f, "eps must be finite and >= 0");
+  const int smem = cfg->num_q_heads * msa::QKR_D * 2;
+  CHECK_SUP(smem <= 200 * 1024, "too many query heads");
+  CHECK_SUP(static_cast<int64_t>(batch->num_seqs) + batch->total_q < (1LL << 31) / (cfg->num_kv_heads + 1),
+            "too many sequences and rows");
+  if (batch->total_q == 0) return MSA_OK;
+  const msa::RopeTable tab = rope_table(rotary_dim, rope_theta);
+  msa::KvInsertArgs a{};
+  a.k_new = static_cast<const __nv_bfloat16*>(k_new);
+  a.v_new = static_cast<const __nv_bfloat16*>(v_new);
+  a.k_w = static_cast<const __nv_bfloat16*>(k_norm_w);
+  a.k_cache = static_cast<uint8_t*>(k_cache_e4m3);
+  a.v_cache = static_cast<uint8_t*>(v_cache_e4m3);
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.q_start = batch->q_start;
+  a.ctx_len = batch->ctx_len;
+  a.page_table = batch->page_table;
+  a.num_seqs = batch->num_seqs;
+  a.total_q = batch->total_q;
+  a.Hkv = cfg->num_kv_heads;
+  a.max_blocks = batch->max_blocks_per_seq;
+  a.num_pages = batch->num_pages;
+  a.rotary_dim = rotary_dim;
+  a.eps = eps;
+  const unsigned pieces = static_cast<unsigned>(batch->num_seqs) + (static_cast<unsigned>(batch->total_q) + 127u) / 128u;
+  msa::kv_insert_fp8_kernel<<<pieces * a.Hkv, msa::KVI_THREADS, 0, stream>>>(a, tab);
+  if ((st = launched()) != MSA_OK) return st;
+  msa::QNormRopeArgs qa{};
+  qa.q = static_cast<const __nv_bfloat16*>(q);
+  qa.q_out = static_cast<__nv_bfloat16*>(q_out);
+  qa.q_w = static_cast<const __nv_bfloat16*>(q_norm_w);
+  qa.q_start = batch->q_start;
+  qa.ctx_len = batch->ctx_len;
+  qa.num_seqs = batch->num_seqs;
+  qa.total_q = batch->total_q;
+  qa.Hq = cfg->num_q_heads;
+  qa.rotary_dim = rotary_dim;
+  qa.eps = eps;
+  CUDA_TRY(set_smem(msa::q_norm_rope_kernel, smem));
+  CUDA_TRY(cudaFuncSetAttribute(msa::q_norm_rope_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                cudaSharedmemCarveoutMaxShared));
+  msa::q_norm_rope_kernel<<<static_cast<unsigned>(batch->total_q), msa::QKR_THREADS, smem, stream>>>(qa, tab);
+  return launched();
+}
+
+msa_status_t msa_advance_batch(int32_t num_seqs, int32_t max_blocks_per_seq, int32_t num_pages, int32_t block_size,
+                               const int32_t* delta, const int32_t* ctx_len, int32_t* page_table, int32_t* free_ring,
+                               const int32_t* pool, int32_t* ctx_len_out, int32_t* pool_out, int32_t* q_start,
+                               int32_t* slot_map, int32_t max_rows, cudaStream_t stream) {
+  CHECK_ARG(num_seqs > 0 && max_blocks_per_seq > 0 && num_pages > 0,
+            "num_seqs, max_blocks_per_seq and num_pages must be positive");
+  CHECK_SUP(num_seqs <= msa::ADV_MAXSEQ, "at most %d sequences per call", msa::ADV_MAXSEQ);
+  CHECK_SUP(max_blocks_per_seq <= 16384, "max_blocks_per_seq must be <= 16384");
+  CHECK_SUP(block_size == 128, "block_size must be 128");
+  CHECK_SUP(num_pages < (1 << 24), "num_pages must be < 2^24");
+  CHECK_ARG(delta && ctx_len && page_table && free_ring && pool && ctx_len_out && pool_out && q_start,
+            "delta, ctx_len, page_table, free_ring, pool, their outputs and q_start must not be NULL");
+  CHECK_ARG(max_rows >= 0 && (slot_map != nullptr || max_rows == 0), "max_rows must be >= 0, and 0 without a slot map");
+  CHECK_ARG(aligned4(delta) && aligned4(ctx_len) && aligned4(page_table) && aligned4(free_ring) && aligned4(pool) &&
+                aligned4(ctx_len_out) && aligned4(pool_out) && aligned4(q_start) && aligned4(slot_map),
+            "pointers must be 4-byte aligned");
+  msa::AdvanceArgs a{};
+  a.delta = delta;
+  a.ctx_len = ctx_len;
+  a.page_table = page_table;
+  a.ring = free_ring;
+  a.pool = pool;
+  a.ctx_out = ctx_len_out;
+  a.pool_out = pool_out;
+  a.q_start = q_start;
+  a.slot_map = slot_map;
+  a.num_seqs = num_seqs;
+  a.max_blocks = max_blocks_per_seq;
+  a.num_pages = num_pages;
+  a.max_rows = max_rows;
+  const int smem = msa::advance_smem(num_seqs);
+  CUDA_TRY(set_smem(msa::advance_batch_kernel, smem));
+  msa::advance_batch_kernel<<<1, msa::ADV_THREADS, smem, stream>>>(a);
+  return launched();
+}
+
+}  // extern "C"

@@ -267,6 +267,94 @@ msa_status_t msa_qknorm_rope_insert(const msa_config_t* cfg, const msa_batch_t* 
 msa_status_t msa_merge_partials(int32_t n, int64_t units, int32_t head_dim, const void* outs, const float* lses,
                                 void* out, float* lse, cudaStream_t stream);
 
+/*
+ * The K/V cache in 8 bits.  The pages list "FP8 KV-cache paths" among the
+ * upcoming work (daily.dev "MiniMax M3 ...", section "What's coming") and fix
+ * no format; this library holds K and V as e4m3 ("fn") codes with one fp32
+ * scale for each page and KV head, i.e. for each block of 128 tokens of a head:
+ *   k_cache_e4m3  uint8 [num_pages][num_kv_heads][block_size][head_dim]   (v_cache_e4m3 alike)
+ *   k_scale       fp32  [num_pages][num_kv_heads]                         (v_scale alike)
+ *   key value = code * k_scale[page][g]
+ * Any finite scale is read; msa_qknorm_rope_insert_fp8 writes powers of two.
+ * Unlike the bf16 caches, slots past a sequence's ctx_len may hold any bytes.
+ *
+ * msa_attn_decode_fp8 / msa_attn_prefill_fp8: the results of msa_attn_decode /
+ * msa_attn_prefill on the values of such a cache, for few and for many queries
+ * per sequence (either takes any batch).  Rows whose selection leaves no key
+ * (all -1) get out = 0 and lse = -inf; rows t >= q_start[num_seqs] (a batch
+ * padded to total_q) are left as they were.  A selected NaN code makes the
+ * results of its row NaN.  A selected block whose id or page is out of range is
+ * recorded as MSA_ERR_DEVICE_BOUNDS and left out.  `workspace` must hold
+ * msa_decode_fp8_workspace_bytes / msa_prefill_fp8_workspace_bytes bytes;
+ * nothing in it needs to be initialised, and calls that may overlap on the GPU
+ * need one each.
+ */
+msa_status_t msa_attn_decode_fp8(const msa_config_t* cfg, const msa_batch_t* batch, const void* q,
+                                 const void* k_cache_e4m3, const void* v_cache_e4m3, const float* k_scale,
+                                 const float* v_scale, const int32_t* block_idx, void* out, float* lse,
+                                 void* workspace, size_t workspace_bytes, cudaStream_t stream);
+msa_status_t msa_attn_prefill_fp8(const msa_config_t* cfg, const msa_batch_t* batch, const void* q,
+                                  const void* k_cache_e4m3, const void* v_cache_e4m3, const float* k_scale,
+                                  const float* v_scale, const int32_t* block_idx, void* out, float* lse,
+                                  void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * msa_qknorm_rope_insert into an 8-bit cache.  Queries as there, written to
+ * q_out (q itself or a disjoint buffer).  New keys (after norm and rope) and
+ * values are rounded once, from fp32, to codes of their page's scale:
+ *   a = the largest finite |new value| that the call writes to (page, g), fit(a) =
+ *   the least power of two s with 448 s >= a (2^-126 at least); then
+ *   scale = fit(a)          if the call writes the page's slot 0 (the page begins anew)
+ *         = the old scale   otherwise, if a <= 448 * old scale
+ *         = fit(a)          otherwise, and the page's earlier slots become
+ *                           e4m3(code * old / new): exact for codes that stay normal
+ *                           where the old scale is a power of two
+ *   code = e4m3(clamp(value / scale, -448, 448)), nearest even; infinities
+ *   saturate, NaN stays NaN.  An old scale that is not positive counts as 0.
+ * Slots behind the last new row, and other pages, are left as they were, and so
+ * are the q_out rows t >= q_start[num_seqs] of a padded batch.  The sequences of
+ * a call must not write to a common page, and k_new / v_new must not overlap
+ * the caches, the scales or q_out.  A page id out of range is recorded as
+ * MSA_ERR_DEVICE_BOUNDS and its rows' cache writes are skipped.
+ */
+msa_status_t msa_qknorm_rope_insert_fp8(const msa_config_t* cfg, const msa_batch_t* batch, const void* q,
+                                        const void* k_new, const void* v_new, const void* q_norm_w,
+                                        const void* k_norm_w, void* q_out, void* k_cache_e4m3, void* v_cache_e4m3,
+                                        float* k_scale, float* v_scale, int32_t rotary_dim, float rope_theta,
+                                        float eps, cudaStream_t stream);
+
+/*
+ * The index arrays of a step from the requests' token counts, on the device (so
+ * that a step needs no host copy and can be replayed as a graph).  Sequence s
+ * holds ctx_len[s] tokens in the pages page_table[s][0 .. ceil(ctx_len[s] / 128) - 1].
+ *   delta     int32 [num_seqs]: > 0 appends that many tokens (this step's query
+ *             rows), < 0 takes tokens back (rejected drafts; -ctx_len[s] ends a
+ *             request), 0 leaves the sequence out of the step
+ *   free_ring int32 [num_pages]: ring of free page ids; pool int32 [4]: {head,
+ *             count, -, -}: the free pages are free_ring[(head + i) % num_pages], i < count
+ * Pages that sequences come to need leave the ring at its head, pages that they no
+ * longer need come back at its tail, both in the order of (sequence, block); pages
+ * given back are not taken in the same call.  Written:
+ *   ctx_len_out[s] = ctx_len[s] + delta[s]      (may be ctx_len itself)
+ *   page_table[s][b] of the new blocks; entries past a sequence's blocks keep what
+ *             they held and are not read again before they are written
+ *   q_start   int32 [num_seqs + 1] = exclusive sum of max(delta, 0)
+ *   slot_map  int32 [max_rows] (NULL with max_rows = 0: not wanted): the cache slot
+ *             page * 128 + position % 128 of each new row, -1 behind the last one
+ *   pool_out  int32 [4] (may be pool itself) = {head, count, 0, number of rows}
+ * q_start, ctx_len_out and page_table then serve as the batch of the other calls.
+ * All or nothing: if the step needs more pages than are free, pool_out = {head,
+ * count, missing pages, 0}, q_start = 0, slot_map = -1 and nothing else changes.
+ * A length below 0 or above max_blocks_per_seq * 128, a ring state out of range or
+ * overfull, or more than max_rows rows end the same way with -1 for the missing
+ * pages, and are recorded as MSA_ERR_DEVICE_BOUNDS, as is a page id out of range
+ * met on the way (it is written as -1).  num_seqs <= 8192, block_size 128.
+ */
+msa_status_t msa_advance_batch(int32_t num_seqs, int32_t max_blocks_per_seq, int32_t num_pages, int32_t block_size,
+                               const int32_t* delta, const int32_t* ctx_len, int32_t* page_table, int32_t* free_ring,
+                               const int32_t* pool, int32_t* ctx_len_out, int32_t* pool_out, int32_t* q_start,
+                               int32_t* slot_map, int32_t max_rows, cudaStream_t stream);
+
 /* Timing hook (no counterpart on the pages).  With n = 4 and four cudaEvent_t
  * handles (owned by the caller), every later msa_attn_prefill call on this host
  * thread records events[0] before its schedule kernels, events[1] before the
@@ -279,6 +367,9 @@ msa_status_t msa_set_timing_events(void* const* events, int32_t n);
  * `batch` are read.  0 means the arguments are invalid. */
 size_t msa_prefill_workspace_bytes(const msa_config_t* cfg, const msa_batch_t* batch);
 size_t msa_decode_workspace_bytes(const msa_config_t* cfg, const msa_batch_t* batch);
+/* The same for the attention calls over the 8-bit cache. */
+size_t msa_prefill_fp8_workspace_bytes(const msa_config_t* cfg, const msa_batch_t* batch);
+size_t msa_decode_fp8_workspace_bytes(const msa_config_t* cfg, const msa_batch_t* batch);
 
 /* Synchronises `stream`, then reads and clears the current device's error
  * word: MSA_OK, MSA_ERR_TIMEOUT or MSA_ERR_DEVICE_BOUNDS (MSA_ERR_CUDA if the
