@@ -13,6 +13,7 @@
 #include "../../include/msa.h"
 #include "advance_batch.cuh"
 #include "attn_decode.cuh"
+#include "attn_decode_fp8.cuh"
 #include "attn_fp8.cuh"
 #include "attn_prefill.cuh"
 #include "common.cuh"
@@ -820,6 +821,31 @@ msa_status_t run_attn_fp8(const msa_config_t* cfg, const msa_batch_t* batch, con
   return launched();
 }
 
+// A launch that may begin while the kernel before it in the stream still runs (which lets it, and for whose end the
+// launched kernel waits on the device).
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream, A... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(grid);
+  c.blockDim = dim3(block);
+  c.dynamicSmemBytes = smem;
+  c.stream = stream;
+  c.attrs = attr;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
+}
+
+// TMA map of an 8-bit K or V cache as [pages * Hkv * 128][128] codes, one block a copy
+msa_status_t make_code_map(CUtensorMap* m, const void* cache, const msa_config_t* cfg, const msa_batch_t* batch) {
+  const uint64_t dims[2] = {128, static_cast<uint64_t>(batch->num_pages) * cfg->num_kv_heads * 128};
+  const uint64_t strides[1] = {128};
+  const uint32_t box[2] = {128, 128};
+  return make_map(m, cache, 2, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8);
+}
+
 // theta^(-2i/r) / (2 pi) for the rotation pairs
 msa::RopeTable rope_table(int rotary_dim, float theta) {
   msa::RopeTable t{};
@@ -834,7 +860,7 @@ extern "C" {
 
 size_t msa_decode_fp8_workspace_bytes(const msa_config_t* cfg, const msa_batch_t* batch) {
   if (check_config(cfg) != MSA_OK || check_batch(batch) != MSA_OK) return 0;
-  return 256;
+  return static_cast<size_t>(msa::ATD8_GRID) * 2 * msa::ATD8_PART * 4;
 }
 
 size_t msa_prefill_fp8_workspace_bytes(const msa_config_t* cfg, const msa_batch_t* batch) {
@@ -849,7 +875,36 @@ msa_status_t msa_attn_decode_fp8(const msa_config_t* cfg, const msa_batch_t* bat
   msa_status_t st = check_attn_fp8(cfg, batch, q, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale, block_idx, out, lse,
                                    workspace, workspace_bytes, msa_decode_fp8_workspace_bytes(cfg, batch));
   if (st != MSA_OK || batch->total_q == 0) return st;
-  return run_attn_fp8(cfg, batch, q, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale, block_idx, out, lse, stream);
+  msa::AttnDecodeFp8Args a{};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.block_idx = block_idx;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  a.q_start = batch->q_start;
+  a.ctx_len = batch->ctx_len;
+  a.page_table = batch->page_table;
+  a.part = static_cast<float*>(workspace);
+  a.num_seqs = batch->num_seqs;
+  a.Hq = cfg->num_q_heads;
+  a.Hkv = cfg->num_kv_heads;
+  a.topk = cfg->topk;
+  a.max_blocks = batch->max_blocks_per_seq;
+  a.num_pages = batch->num_pages;
+  a.n_slots = batch->total_q * cfg->num_kv_heads * cfg->topk;   // < 2^31 (checked)
+  a.total_q = batch->total_q;
+  a.once = batch->max_q_per_seq == 1;
+  a.scale_log2 = softmax_scale(cfg) * 1.4426950408889634f;
+  CUtensorMap tk, tv;
+  if ((st = make_code_map(&tk, k_cache_e4m3, cfg, batch)) != MSA_OK) return st;
+  if ((st = make_code_map(&tv, v_cache_e4m3, cfg, batch)) != MSA_OK) return st;
+  CUDA_TRY(set_smem(msa::attn_decode_fp8_kernel, msa::ATD8_SMEM));
+  const int grid = std::min(a.n_slots, msa::ATD8_GRID);
+  msa::attn_decode_fp8_kernel<<<grid, msa::ATD8_THREADS, msa::ATD8_SMEM, stream>>>(tk, tv, a);
+  if ((st = launched()) != MSA_OK || grid == 1) return st;
+  CUDA_TRY(launch_overlapped(msa::attn_decode_fp8_merge_kernel, grid - 1, 256, 0, stream, a, grid));
+  return MSA_OK;
 }
 
 msa_status_t msa_attn_prefill_fp8(const msa_config_t* cfg, const msa_batch_t* batch, const void* q,
