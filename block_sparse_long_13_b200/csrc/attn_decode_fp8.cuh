@@ -25,8 +25,8 @@
 // blocks whatever the batch (whole rows per CTA would leave 64 x 4 groups two rounds over 148 CTAs: 0.86 busy).  A
 // (row, group) that a border cuts leaves partial sums, which attn_decode_fp8_merge_kernel joins.
 //
-// Warps: 0 issues the copies (6 stages of K + V tiles, 192 KiB in flight), 1 the MMAs, 2 splits the queries, 3 looks
-// up slots (32 at a time: block id, sequence, page, scales), 4-7 run the softmax (thread = key; running maxima over
+// Warps: 0 issues the copies (6 stages of K + V tiles, 192 KiB in flight), 1 the MMAs of S^T, 12 those of O^T, 2 splits
+// the queries, 3 looks up slots (32 at a time: block id, sequence, page, scales), 4-7 run the softmax (thread = key; running maxima over
 // the row's blocks, so a block's probabilities have the scale of the row so far), 8-11 keep the output (thread =
 // dim): acc = acc 2^(M_old - M) + vs_b O_b.  Every wait is bounded.
 #pragma once
@@ -35,7 +35,7 @@
 
 namespace msa {
 
-constexpr int ATD8_THREADS = 384;
+constexpr int ATD8_THREADS = 416;
 constexpr int ATD8_GRID = 148;         // CTAs at most
 constexpr int ATD8_STAGES = 6;         // K + V tiles of a block
 constexpr int ATD8_TILE = 16384;       // one K or V block: [128 keys][128 dims] codes, 128-byte swizzle
@@ -43,7 +43,7 @@ constexpr int ATD8_RING = 4;           // S^T and O^T accumulators (TMEM), P^T t
 constexpr int ATD8_PT = 4096;          // P^T or Q of a row: [high, low][2 KiB]
 constexpr int ATD8_BATCHES = 4;        // slot records in flight, 32 each
 constexpr int ATD8_SMEM = ATD8_STAGES * 2 * ATD8_TILE + ATD8_RING * ATD8_PT + 2 * ATD8_PT + 1024;
-constexpr uint32_t ATD8_TM_S = 0, ATD8_TM_O = ATD8_RING * 16, ATD8_TMEM = 128;
+constexpr uint32_t ATD8_TM_S = 0, ATD8_TM_O = ATD8_RING * 32, ATD8_TMEM = 256;   // S^T: 32 columns (high, low part), O^T: 16
 constexpr int ATD8_PART = 16 * 128 + 32;   // floats of a partial result: sums [16][128], maxima [16], sums of p [16]
 constexpr float ATD8_LOW = -1e30f;     // start of the running maxima (finite: -inf - -inf is NaN)
 
@@ -126,12 +126,17 @@ attn_decode_fp8_kernel(const __grid_constant__ CUtensorMap tmap_k,    // k codes
   uint8_t* q_s = ring + ATD8_STAGES * 2 * ATD8_TILE;      // 2 x [high, low][16 heads][128] (128-byte swizzle)
   uint8_t* p_s = q_s + 2 * ATD8_PT;                       // ring of [high, low][128 keys][16 heads]
 
+  // Ring slot of block i: s_full S^T is in TMEM; p_full its P^T and factors are in shared memory (and S^T is read);
+  // o_full O^T is in TMEM (and P^T is read); o_empty O^T and the factors are read.  So p_full(i - RING) also says
+  // that S^T(i) may be written, and o_empty(i - RING), which the softmax waits for, that P^T(i) and O^T(i) may be.
   __shared__ uint64_t k_full[ATD8_STAGES], v_full[ATD8_STAGES], kv_empty[ATD8_STAGES], s_full[ATD8_RING],
-      s_empty[ATD8_RING], p_full[ATD8_RING], p_empty[ATD8_RING], o_full[ATD8_RING], o_empty[ATD8_RING],
-      rec_full[ATD8_BATCHES], rec_empty[ATD8_BATCHES], q_full[2], q_empty[2], us_full[2], us_empty[2], drain_bar;
+      p_full[ATD8_RING], o_full[ATD8_RING], o_empty[ATD8_RING], rec_full[ATD8_BATCHES], rec_empty[ATD8_BATCHES],
+      q_full[2], q_empty[2], us_full[2], us_empty[2], drain_bar[2];
   __shared__ __align__(16) int4 s_rec[ATD8_BATCHES * 32]; // slot: TMA row or -1, visible keys, K scale, V scale
+  __shared__ uint32_t s_mask[ATD8_BATCHES];               // slots of the batch that hold a block
   __shared__ __align__(16) float s_fq[2][16];             // softmax scale x log2 e / the query's power of two
   __shared__ __align__(16) float s_red[2][4][16];         // per-warp maxima of a block, by block parity
+  __shared__ __align__(16) float s_run[4][2][16];         // per warp: the row's running maxima, the block's factors
   __shared__ __align__(16) float s_alpha[ATD8_RING][16];  // 2^(M_old - M) of a block
   __shared__ __align__(16) float s_m[2][16], s_l[2][4][16];   // of a finished (row, group): maxima, per-warp sums of p
   __shared__ uint32_t s_tmem;
@@ -153,15 +158,13 @@ attn_decode_fp8_kernel(const __grid_constant__ CUtensorMap tmap_k,    // k codes
     }
     for (int i = 0; i < ATD8_RING; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_empty[i], 4);
       mbar_init(&p_full[i], 4);
-      mbar_init(&p_empty[i], 1);
       mbar_init(&o_full[i], 1);
       mbar_init(&o_empty[i], 4);
     }
     for (int i = 0; i < ATD8_BATCHES; ++i) {
       mbar_init(&rec_full[i], 1);
-      mbar_init(&rec_empty[i], 10);                       // producer, issuer, 4 softmax and 4 output warps
+      mbar_init(&rec_empty[i], 11);                       // producer, two issuers, 4 softmax and 4 output warps
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
@@ -169,7 +172,8 @@ attn_decode_fp8_kernel(const __grid_constant__ CUtensorMap tmap_k,    // k codes
       mbar_init(&us_full[i], 4);
       mbar_init(&us_empty[i], 4);
     }
-    mbar_init(&drain_bar, 1);
+    mbar_init(&drain_bar[0], 1);
+    mbar_init(&drain_bar[1], 1);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -186,7 +190,8 @@ attn_decode_fp8_kernel(const __grid_constant__ CUtensorMap tmap_k,    // k codes
     const int rb = bt & (ATD8_BATCHES - 1);
     if (!mbar_wait_warp(&rec_full[rb], (bt / ATD8_BATCHES) & 1, &s_abort)) return false;
     r = s_rec[rb * 32 + lane];
-    mask = __ballot_sync(0xFFFFFFFFu, r.x >= 0);
+    mask = s_mask[rb];
+    __syncwarp();
     if (lane == 0) mbar_arrive(&rec_empty[rb]);
     return true;
   };
@@ -216,6 +221,8 @@ attn_decode_fp8_kernel(const __grid_constant__ CUtensorMap tmap_k,    // k codes
       const int rb = bt & (ATD8_BATCHES - 1);
       if (!mbar_wait_warp(&rec_empty[rb], ((bt / ATD8_BATCHES) & 1) ^ 1, &s_abort)) break;
       s_rec[rb * 32 + lane] = rec;
+      const uint32_t mask = __ballot_sync(0xFFFFFFFFu, rec.x >= 0);
+      if (lane == 0) s_mask[rb] = mask;
       __syncwarp();
       if (lane == 0) mbar_arrive(&rec_full[rb]);
     }
@@ -259,76 +266,88 @@ attn_decode_fp8_kernel(const __grid_constant__ CUtensorMap tmap_k,    // k codes
       }
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMAs: S_0, (S_i, PV_i-1) ..., PV_last
-    const uint32_t id_s = idesc_e4m3(128, 16, false, false);   // A = K_b (K-major), B = Q (K-major)
-    const uint32_t id_pv = idesc_e4m3(128, 16, true, true);    // A = V_b^T, B = P^T (both MN-major)
-    const uint64_t k_d = sdesc_sw128(smem_u32(ring), 16, 1024);
-    const uint64_t v_d = sdesc_sw128(smem_u32(ring) + ATD8_TILE, ATD8_TILE, 1024);
-    const uint64_t q_d = sdesc_sw128(smem_u32(q_s), 16, 1024);
-    const uint64_t p_d = sdesc_rows16(smem_u32(p_s));
-    int st = 0, ph = 0, pst = 0, pph = 0;    // stage and parity of the next S and of the next PV
-    uint32_t ns = 0, np = 0;
-    int uq = 0, left = left0;
-    bool ok = true, need_q = true;
-    auto wait_q = [&]() -> bool {
-      need_q = false;
-      return mbar_wait_warp(&q_full[uq & 1], (uq >> 1) & 1, &s_abort);
-    };
-    auto issue_pv = [&]() -> bool {
-      const uint32_t ps = np % ATD8_RING, par = (np / ATD8_RING) & 1;
-      if (!mbar_wait_warp(&v_full[pst], pph, &s_abort) || !mbar_wait_warp(&p_full[ps], par, &s_abort) ||
-          !mbar_wait_warp(&o_empty[ps], par ^ 1, &s_abort)) return false;
-      tc_fence_after();
-      if (lane == 0) {
-        const uint64_t vd = v_d + ((pst * 2 * ATD8_TILE) >> 4), pd = p_d + ((ps * ATD8_PT) >> 4);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)       // 32 keys per step: 4 KiB of V rows, 512 bytes of P rows; high, then low part
-          umma_e4m3_ss(tmem + ATD8_TM_O + ps * 16, vd + (kk & 3) * 256, pd + (kk >> 2) * 128 + (kk & 3) * 32, id_pv, kk > 0 ? 1u : 0u);
-        umma_commit(&kv_empty[pst]);
-        umma_commit(&p_empty[ps]);
-        umma_commit(&o_full[ps]);
-      }
-      __syncwarp();
-      ++np;
-      if (++pst == ATD8_STAGES) { pst = 0; pph ^= 1; }
-      return true;
-    };
-    for (int bt = 0; bt < nbatch && ok; ++bt) {
-      int4 r;
-      uint32_t mask;
-      if (!take_batch(bt, r, mask)) { ok = false; break; }
-      const int cnt = min(32, n - bt * 32);
-      for (int j = 0; j < cnt && ok; ++j) {
-        if ((mask >> j) & 1) {
-          const uint32_t ss = ns % ATD8_RING;
-          if ((need_q && !wait_q()) || !mbar_wait_warp(&k_full[st], ph, &s_abort) ||
-              !mbar_wait_warp(&s_empty[ss], ((ns / ATD8_RING) & 1) ^ 1, &s_abort)) { ok = false; break; }
-          tc_fence_after();
-          if (lane == 0) {
+    // ------------------------------------------------------------ S^T = K_b Q^T, one thread
+    // Q's high and low part are the two halves of one N = 32 operand: an MMA this narrow takes 47 clocks whatever its
+    // N (measured, N <= 64), so one pass over K for both halves the MMAs; the softmax adds the halves.
+    if (lane == 0) {
+      const uint32_t id_s = idesc_e4m3(128, 32, false, false);   // A = K_b (K-major), B = Q (K-major)
+      const uint64_t k_d = sdesc_sw128(smem_u32(ring), 16, 1024);
+      const uint64_t q_d = sdesc_sw128(smem_u32(q_s), 16, 1024);
+      int st = 0, ph = 0, left = left0, uq = 0;
+      uint32_t ns = 0;
+      bool ok = true, need_q = true;
+      for (int bt = 0; bt < nbatch && ok; ++bt) {
+        const int rb = bt & (ATD8_BATCHES - 1);
+        if (!mbar_wait(&rec_full[rb], (bt / ATD8_BATCHES) & 1, &s_abort)) break;
+        const uint32_t mask = s_mask[rb];
+        mbar_arrive(&rec_empty[rb]);
+        const int cnt = min(32, n - bt * 32);
+        for (int j = 0; j < cnt && ok; ++j) {
+          const bool ends = --left == 0 || bt * 32 + j == n - 1;
+          if (need_q && (((mask >> j) & 1) || ends)) {
+            ok = mbar_wait(&q_full[uq & 1], (uq >> 1) & 1, &s_abort);
+            need_q = false;
+          }
+          if (ok && ((mask >> j) & 1)) {
+            const uint32_t ss = ns % ATD8_RING;
+            ok = mbar_wait(&k_full[st], ph, &s_abort) &&
+                 (ns < ATD8_RING || mbar_wait(&p_full[ss], (ns / ATD8_RING - 1) & 1, &s_abort));
+            if (!ok) break;
+            tc_fence_after();
             const uint64_t kd = k_d + ((st * 2 * ATD8_TILE) >> 4), qd = q_d + (((uq & 1) * ATD8_PT) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)   // 32 dims per step, within a 128-byte row; high, then low part
-              umma_e4m3_ss(tmem + ATD8_TM_S + ss * 16, kd + (kk & 3) * 2, qd + (kk >> 2) * 128 + (kk & 3) * 2, id_s, kk > 0 ? 1u : 0u);
+            for (int kk = 0; kk < 4; ++kk)   // 32 dims per step, within a 128-byte row
+              umma_e4m3_ss(tmem + ATD8_TM_S + ss * 32, kd + kk * 2, qd + kk * 2, id_s, kk > 0 ? 1u : 0u);
             umma_commit(&s_full[ss]);
+            ++ns;
+            if (++st == ATD8_STAGES) { st = 0; ph ^= 1; }
           }
-          __syncwarp();
-          ++ns;
-          if (++st == ATD8_STAGES) { st = 0; ph ^= 1; }
-          if (ns > np + 1) ok = issue_pv();
-        }
-        if (--left == 0 || bt * 32 + j == n - 1) {
-          if (!ok || (need_q && !wait_q())) { ok = false; break; }
-          if (lane == 0) umma_commit(&q_empty[uq & 1]);
-          ++uq;
-          need_q = true;
-          left = a.topk;
+          if (ends && ok) {
+            umma_commit(&q_empty[uq & 1]);
+            ++uq;
+            need_q = true;
+            left = a.topk;
+          }
         }
       }
+      if (s_abort) {
+        umma_commit(&drain_bar[0]);
+        mbar_wait_drain(&drain_bar[0], 0);
+      }
     }
-    if (ok && ns > np) issue_pv();
-    if (lane == 0 && s_abort) {
-      umma_commit(&drain_bar);
-      mbar_wait_drain(&drain_bar, 0);
+  } else if (warp == 12) {
+    // ------------------------------------------------------------ O_b^T = V_b^T P^T, one thread
+    if (lane == 0) {
+      const uint32_t id_pv = idesc_e4m3(128, 16, true, true);    // A = V_b^T, B = P^T (both MN-major)
+      const uint64_t v_d = sdesc_sw128(smem_u32(ring) + ATD8_TILE, ATD8_TILE, 1024);
+      const uint64_t p_d = sdesc_rows16(smem_u32(p_s));
+      int st = 0, ph = 0;
+      uint32_t np = 0;
+      bool ok = true;
+      for (int bt = 0; bt < nbatch && ok; ++bt) {
+        const int rb = bt & (ATD8_BATCHES - 1);
+        if (!mbar_wait(&rec_full[rb], (bt / ATD8_BATCHES) & 1, &s_abort)) break;
+        const int cnt = __popc(s_mask[rb]);
+        mbar_arrive(&rec_empty[rb]);
+        for (int j = 0; j < cnt; ++j) {
+          const uint32_t ps = np % ATD8_RING;
+          ok = mbar_wait(&v_full[st], ph, &s_abort) && mbar_wait(&p_full[ps], (np / ATD8_RING) & 1, &s_abort);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t vd = v_d + ((st * 2 * ATD8_TILE) >> 4), pd = p_d + ((ps * ATD8_PT) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)     // 32 keys per step: 4 KiB of V rows, 512 bytes of P rows; high, then low part
+            umma_e4m3_ss(tmem + ATD8_TM_O + ps * 16, vd + (kk & 3) * 256, pd + (kk >> 2) * 128 + (kk & 3) * 32, id_pv, kk > 0 ? 1u : 0u);
+          umma_commit(&o_full[ps]);
+          umma_commit(&kv_empty[st]);
+          ++np;
+          if (++st == ATD8_STAGES) { st = 0; ph ^= 1; }
+        }
+      }
+      if (s_abort) {
+        umma_commit(&drain_bar[1]);
+        mbar_wait_drain(&drain_bar[1], 0);
+      }
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------ queries: lane = half a head
@@ -385,16 +404,17 @@ attn_decode_fp8_kernel(const __grid_constant__ CUtensorMap tmap_k,    // k codes
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[qb]);
     }
-  } else if (warp < 8) {
+  } else if (warp >= 4 && warp < 8) {
     // ------------------------------------------------------------ softmax: thread = key
     // The four warps meet at one barrier a block (the exchange of their maxima), which also carries a failed wait
     // to all of them: after a failed wait a warp goes to that barrier and leaves, and so do the others there or at
     // the last barrier, behind the last slot.
     const int sw = warp - 4, row = sw * 32 + lane;
     const uint32_t s_addr = tmem + (static_cast<uint32_t>(sw * 32) << 16) + ATD8_TM_S;
-    float M[16], L[16], fq[16];
+    // Lane h (and h + 16) keeps the running maximum of head h; the sums are per thread, i.e. per key.
+    float mine = ATD8_LOW, L[16], fq[16];
 #pragma unroll
-    for (int h = 0; h < 16; ++h) { M[h] = ATD8_LOW; L[h] = 0.f; }
+    for (int h = 0; h < 16; ++h) L[h] = 0.f;
     int st = 0, ph = 0;                      // the block's stage
     uint32_t nb = 0;
     int u = 0, left = left0;
@@ -426,15 +446,14 @@ attn_decode_fp8_kernel(const __grid_constant__ CUtensorMap tmap_k,    // k codes
           float x[16];
           if (ok) {
             tc_fence_after();
-            tmem_ld16(s_addr + ss * 16, x);
+            float v[32];
+            tmem_ld32(s_addr + ss * 32, v);
             tmem_ld_wait();
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s_empty[ss]);
             float wm[16];
 #pragma unroll
             for (int h = 0; h < 16; ++h) {
-              x[h] = row < nvis ? x[h] * (fq[h] * ks) : -INFINITY;
+              x[h] = row < nvis ? (v[h] + v[16 + h]) * (fq[h] * ks) : -INFINITY;
               wm[h] = warp_max(x[h]);
             }
             if (lane == 0) {
@@ -442,42 +461,36 @@ attn_decode_fp8_kernel(const __grid_constant__ CUtensorMap tmap_k,    // k codes
 #pragma unroll
               for (int i = 0; i < 4; ++i) d[i] = make_float4(wm[4 * i], wm[4 * i + 1], wm[4 * i + 2], wm[4 * i + 3]);
             }
-            // P^T tile and rescaling factors of the block RING back are read
-            ok = mbar_wait_warp(&p_empty[ss], par ^ 1, &s_abort) && mbar_wait_warp(&o_empty[ss], par ^ 1, &s_abort);
+            // the P^T tile and the factors of the block RING back are read
+            ok = mbar_wait_warp(&o_empty[ss], par ^ 1, &s_abort);
           }
           if (named_bar_any(1, 128, !ok)) { left_group = true; break; }
-          float al[16];
-          bool grown = false;
+          // every warp joins the four maxima for itself, a head per lane, and hands them to its lanes
+          const float(&red)[4][16] = s_red[nb & 1];
+          const int h16 = lane & 15;
+          const float bm = fmaxf(fmaxf(red[0][h16], red[1][h16]), fmaxf(red[2][h16], red[3][h16]));
+          const float old = mine;
+          mine = fmaxf(old, bm);
+          const float fac = exp2f(old - mine);
+          if (lane < 16) {
+            s_run[sw][0][lane] = mine;
+            s_run[sw][1][lane] = fac;
+            if (sw == 0) s_alpha[ss][lane] = fac;
+          }
+          const bool grown = __any_sync(0xFFFFFFFFu, mine > old);
+          __syncwarp();
+          float M[16];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float4 m = *reinterpret_cast<const float4*>(&s_red[nb & 1][0][4 * i]);
-#pragma unroll
-            for (int w = 1; w < 4; ++w) {
-              const float4 o = *reinterpret_cast<const float4*>(&s_red[nb & 1][w][4 * i]);
-              m.x = fmaxf(m.x, o.x); m.y = fmaxf(m.y, o.y); m.z = fmaxf(m.z, o.z); m.w = fmaxf(m.w, o.w);
-            }
-            const float mm[4] = {m.x, m.y, m.z, m.w};
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              const float old = M[4 * i + v];
-              M[4 * i + v] = fmaxf(old, mm[v]);
-              al[4 * i + v] = old - M[4 * i + v];
-              grown |= mm[v] > old;
-            }
+            const float4 m = *reinterpret_cast<const float4*>(&s_run[sw][0][4 * i]);
+            M[4 * i] = m.x; M[4 * i + 1] = m.y; M[4 * i + 2] = m.z; M[4 * i + 3] = m.w;
           }
-          if (grown) {                       // uniform over the group
+          if (grown) {
 #pragma unroll
-            for (int h = 0; h < 16; ++h) { al[h] = exp2f(al[h]); L[h] *= al[h]; }
-          } else {
-#pragma unroll
-            for (int h = 0; h < 16; ++h) al[h] = 1.f;
-          }
-          if (lane == 0) {                   // warp sw writes the factors of heads 4 sw ..
-            float4* d = reinterpret_cast<float4*>(&s_alpha[ss][4 * sw]);
-            if (sw == 0) *d = make_float4(al[0], al[1], al[2], al[3]);
-            else if (sw == 1) *d = make_float4(al[4], al[5], al[6], al[7]);
-            else if (sw == 2) *d = make_float4(al[8], al[9], al[10], al[11]);
-            else *d = make_float4(al[12], al[13], al[14], al[15]);
+            for (int i = 0; i < 4; ++i) {
+              const float4 f = *reinterpret_cast<const float4*>(&s_run[sw][1][4 * i]);
+              L[4 * i] *= f.x; L[4 * i + 1] *= f.y; L[4 * i + 2] *= f.z; L[4 * i + 3] *= f.w;
+            }
           }
           uint32_t hi[4], lw[4];
 #pragma unroll
@@ -485,7 +498,7 @@ attn_decode_fp8_kernel(const __grid_constant__ CUtensorMap tmap_k,    // k codes
             float p[4];
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-              p[v] = exp2f(x[4 * i + v] - (M[4 * i + v] - 8.f));     // 256 2^(x - M); 2^-inf = 0
+              p[v] = exp2f((x[4 * i + v] - M[4 * i + v]) + 8.f);     // 256 2^(x - M); 2^-inf = 0
               L[4 * i + v] += p[v];
             }
             uint32_t h0, l0, h1, l1;
@@ -518,14 +531,12 @@ attn_decode_fp8_kernel(const __grid_constant__ CUtensorMap tmap_k,    // k codes
           if (!ok) break;
           const float ws = warp_reduce16<false>(L, lane);
           if ((lane & 1) == 0) s_l[u & 1][sw][lane >> 1] = ws;
-          if (sw == 0 && lane == 0) {
-#pragma unroll
-            for (int h = 0; h < 16; ++h) s_m[u & 1][h] = M[h];
-          }
+          if (sw == 0 && lane < 16) s_m[u & 1][lane] = mine;
           __syncwarp();
           if (lane == 0) mbar_arrive(&us_full[u & 1]);
+          mine = ATD8_LOW;
 #pragma unroll
-          for (int h = 0; h < 16; ++h) { M[h] = ATD8_LOW; L[h] = 0.f; }
+          for (int h = 0; h < 16; ++h) L[h] = 0.f;
           ++u;
           need_q = true;
           left = a.topk;
