@@ -892,15 +892,17 @@ msa_status_t msa_attn_decode_fp8(const msa_config_t* cfg, const msa_batch_t* bat
   a.topk = cfg->topk;
   a.max_blocks = batch->max_blocks_per_seq;
   a.num_pages = batch->num_pages;
-  a.n_slots = batch->total_q * cfg->num_kv_heads * cfg->topk;   // < 2^31 (checked)
-  a.total_q = batch->total_q;
+  const int n_slots = batch->total_q * cfg->num_kv_heads * cfg->topk;   // < 2^31 (checked)
+  const int grid = std::min(n_slots, msa::ATD8_GRID);
+  a.per = n_slots / grid;
+  a.extra = n_slots % grid;
+  a.rows_per_seq = std::max(1, batch->total_q / batch->num_seqs);
   a.once = batch->max_q_per_seq == 1;
   a.scale_log2 = softmax_scale(cfg) * 1.4426950408889634f;
   CUtensorMap tk, tv;
   if ((st = make_code_map(&tk, k_cache_e4m3, cfg, batch)) != MSA_OK) return st;
   if ((st = make_code_map(&tv, v_cache_e4m3, cfg, batch)) != MSA_OK) return st;
   CUDA_TRY(set_smem(msa::attn_decode_fp8_kernel, msa::ATD8_SMEM));
-  const int grid = std::min(a.n_slots, msa::ATD8_GRID);
   msa::attn_decode_fp8_kernel<<<grid, msa::ATD8_THREADS, msa::ATD8_SMEM, stream>>>(tk, tv, a);
   if ((st = launched()) != MSA_OK || grid == 1) return st;
   CUDA_TRY(launch_overlapped(msa::attn_decode_fp8_merge_kernel, grid - 1, 256, 0, stream, a, grid));
