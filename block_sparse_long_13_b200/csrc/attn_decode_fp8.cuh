@@ -132,6 +132,37 @@ __device__ __forceinline__ void e4m3x2_split(float a, float b, uint32_t& hi, uin
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// A head's queries come to (224, 448] times 2^k, 448 = 1.75 * 2^8, by the largest of them (|q| as bf16 bits: NaN above
+// infinity above the rest).
+__device__ __forceinline__ uint32_t abs_max_bf16(const uint4& x) {
+  const uint32_t m = __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+  return max(m & 0xFFFFu, m >> 16);
+}
+__device__ __forceinline__ int query_exponent(uint32_t m) {
+  return min(120, 135 - static_cast<int>(m >> 7) - ((m & 0x7Fu) > 0x60u ? 1 : 0));
+}
+// what the scores of such a head are multiplied by; an infinite or NaN query makes its head NaN
+__device__ __forceinline__ float query_factor(uint32_t m, float scale_log2) {
+  return m >= 0x7F80u ? __uint_as_float(0x7FC00000u)
+                      : scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - query_exponent(m)) << 23);
+}
+// 16 dims (two 16-byte loads) from dim d on of head h into the parts of the Q tile
+__device__ __forceinline__ void split_queries(uint8_t* qt, int h, int d, const uint4& x, const uint4& y, float mult) {
+  const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+  uint32_t hi[4], lw[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t h0, l0, h1, l1;
+    e4m3x2_split(bf16lo(w[2 * i]) * mult, bf16hi(w[2 * i]) * mult, h0, l0);
+    e4m3x2_split(bf16lo(w[2 * i + 1]) * mult, bf16hi(w[2 * i + 1]) * mult, h1, l1);
+    hi[i] = h0 | (h1 << 16);
+    lw[i] = l0 | (l1 << 16);
+  }
+  const uint32_t at = sw128_offset(h, d);
+  *reinterpret_cast<uint4*>(qt + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+  *reinterpret_cast<uint4*>(qt + 2048 + at) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+}
+
 // The sequence of row t: exact at the first look when all sequences have as many rows, a search otherwise.
 __device__ __forceinline__ int find_seq_even(const int32_t* q_start, int num_seqs, int rows_per_seq, int t) {
   const int s = min(num_seqs - 1, t / rows_per_seq);
@@ -192,10 +223,62 @@ attn_decode_fp8_kernel(const __grid_constant__ CUtensorMap tmap_k,    // k codes
       mbar_init(&drain_bar[lane], 1);
     }
     fence_mbar_init();
+    __syncwarp();
+    if (lane == 0) {                         // the first records and queries are written before the block's barrier below
+      mbar_arrive(&rec_full[0]);
+      mbar_arrive(&q_full[0]);
+    }
   }
   if (warp == 1) {
     tmem_alloc(&s_tmem, ATD8_TMEM);
     tmem_relinquish();
+  }
+  // The record of slot lane of batch bt: block id and sequence, then position and page, then the scales, a round trip
+  // each.
+  auto look_up = [&](int bt) -> int4 {
+    int4 rec = make_int4(-1, 0, 0, 0);
+    const int i = lo + bt * 32 + lane;
+    if (bt * 32 + lane < n) {
+      const int b = __ldg(a.block_idx + i);
+      const int unit = i / a.topk, t = unit / a.Hkv, g = unit - t * a.Hkv;
+      const int s = find_seq_even(a.q_start, a.num_seqs, a.rows_per_seq, t);
+      const int end = __ldg(a.q_start + s + 1), ctx = __ldg(a.ctx_len + s);
+      const bool listed = b >= 0 && b < a.max_blocks;
+      const int page = listed ? __ldg(a.page_table + static_cast<long>(s) * a.max_blocks + b) : -1;
+      if (b >= 0 && t < end) {                            // rows behind the last sequence hold nothing
+        const int p = ctx - end + t;
+        if (page >= 0 && page < a.num_pages && b * 128 <= p) {
+          const int tile = page * a.Hkv + g;
+          rec = make_int4(tile * 128, min(128, p - b * 128 + 1), __float_as_int(__ldg(a.k_scale + tile)),
+                          __float_as_int(__ldg(a.v_scale + tile)));
+        } else {
+          flag_error(MSA_DEV_BOUNDS);
+        }
+      }
+    }
+    return rec;
+  };
+  auto q_row = [&](int unit, int h) {
+    const int t = unit / a.Hkv, g = unit - t * a.Hkv;
+    return reinterpret_cast<const uint4*>(a.q + (static_cast<long>(t) * a.Hq + g * 16 + h) * 128);
+  };
+  auto put_batch = [&](int rb, const int4& rec) {
+    s_rec[rb * 32 + lane] = rec;
+    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, rec.x >= 0);
+    if (lane == 0) s_mask[rb] = mask;
+  };
+  // While the barriers are set up: the first records (warp 3) and the first queries (warps 8-11, 8 threads a head).
+  if (warp == 3) {
+    put_batch(0, look_up(0));
+  } else if (warp >= 8 && warp < 12) {
+    const int h = (tid - 256) >> 3, d8 = tid & 7;
+    const uint4 x = __ldg(q_row(unit0, h) + 2 * d8), y = __ldg(q_row(unit0, h) + 2 * d8 + 1);
+    uint32_t m = max(abs_max_bf16(x), abs_max_bf16(y));
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    split_queries(q_s, h, d8 * 16, x, y, __uint_as_float(static_cast<uint32_t>(127 + query_exponent(m)) << 23));
+    if (d8 == 0) s_fq[0][h] = query_factor(m, a.scale_log2);
+    fence_proxy_async_smem();
   }
   tc_fence_before();
   __syncthreads();
@@ -219,84 +302,41 @@ attn_decode_fp8_kernel(const __grid_constant__ CUtensorMap tmap_k,    // k codes
     // (row, group) two before, its blocks and its queries) is out by then.
     const int nu = (lo + n - 1) / a.topk - unit0 + 1;
     const int h = lane >> 1, half = lane & 1;             // queries: half a head a lane
-    auto q_row = [&](int unit) {
-      const int t = unit / a.Hkv, g = unit - t * a.Hkv;
-      return reinterpret_cast<const uint4*>(a.q + (static_cast<long>(t) * a.Hq + g * 16 + h) * 128 + half * 64);
-    };
+    int u = 1;
     uint4 x[8];
+    auto load_q = [&]() {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __ldg(q_row(unit0) + i);
-    int u = 0;
+      for (int i = 0; i < 8; ++i) x[i] = __ldg(q_row(unit0 + u, h) + half * 8 + i);
+    };
+    if (nu > 1) load_q();
     for (int bt = 0; bt < nbatch; ++bt) {
-      int4 rec = make_int4(-1, 0, 0, 0);
-      const int i = lo + bt * 32 + lane;
-      if (bt * 32 + lane < n) {
-        const int b = __ldg(a.block_idx + i);
-        const int unit = i / a.topk, t = unit / a.Hkv, g = unit - t * a.Hkv;
-        const int s = find_seq_even(a.q_start, a.num_seqs, a.rows_per_seq, t);
-        const int p_end = __ldg(a.ctx_len + s), end = __ldg(a.q_start + s + 1);
-        const bool listed = b >= 0 && b < a.max_blocks;
-        const int page = listed ? __ldg(a.page_table + static_cast<long>(s) * a.max_blocks + b) : -1;
-        if (b >= 0 && t < end) {                          // rows behind the last sequence hold nothing
-          const int p = p_end - end + t;
-          if (page >= 0 && page < a.num_pages && b * 128 <= p) {
-            const int tile = page * a.Hkv + g;
-            rec = make_int4(tile * 128, min(128, p - b * 128 + 1), __float_as_int(__ldg(a.k_scale + tile)),
-                            __float_as_int(__ldg(a.v_scale + tile)));
-          } else {
-            flag_error(MSA_DEV_BOUNDS);
-          }
-        }
+      if (bt > 0) {
+        const int4 rec = look_up(bt);
+        const int rb = bt & (ATD8_BATCHES - 1);
+        if (!mbar_wait_soon_warp(&rec_empty[rb], ((bt / ATD8_BATCHES) & 1) ^ 1, &s_abort)) break;
+        put_batch(rb, rec);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&rec_full[rb]);
       }
-      const int rb = bt & (ATD8_BATCHES - 1);
-      if (!mbar_wait_soon_warp(&rec_empty[rb], ((bt / ATD8_BATCHES) & 1) ^ 1, &s_abort)) break;
-      s_rec[rb * 32 + lane] = rec;
-      const uint32_t mask = __ballot_sync(0xFFFFFFFFu, rec.x >= 0);
-      if (lane == 0) s_mask[rb] = mask;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&rec_full[rb]);
       const int begun = min(nu, (lo + min(n, bt * 32 + 32) - 1) / a.topk - unit0 + 1);   // (row, group)s begun so far
       for (; u < begun; ++u) {
-        uint32_t m2 = 0;
+        uint32_t m = 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          m2 = __vmaxu2(m2, __vmaxu2(x[k].x & 0x7FFF7FFFu, x[k].y & 0x7FFF7FFFu));
-          m2 = __vmaxu2(m2, __vmaxu2(x[k].z & 0x7FFF7FFFu, x[k].w & 0x7FFF7FFFu));
-        }
-        uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);         // |largest| as bf16 bits (NaN above infinity above the rest)
+        for (int i = 0; i < 8; ++i) m = max(m, abs_max_bf16(x[i]));
         m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-        // times 2^k: the largest comes to (224, 448], 448 = 1.75 * 2^8
-        const int k = min(120, 135 - static_cast<int>(m >> 7) - ((m & 0x7Fu) > 0x60u ? 1 : 0));
-        const float mult = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+        const float mult = __uint_as_float(static_cast<uint32_t>(127 + query_exponent(m)) << 23);
         const int qb = u & 1;
         if (!mbar_wait_soon_warp(&q_empty[qb], ((u >> 1) & 1) ^ 1, &s_abort)) { bt = nbatch; break; }
-        if (half == 0)
-          s_fq[qb][h] = m >= 0x7F80u ? __uint_as_float(0x7FC00000u)   // an infinite or NaN query: its head is NaN
-                                     : a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-        uint8_t* qt = q_s + qb * ATD8_PT;
+        if (half == 0) s_fq[qb][h] = query_factor(m, a.scale_log2);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {                     // 16 dims: 16 bytes of each part
-          uint32_t hi[4], lw[4];
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const uint4& v = x[2 * c + (w >> 1)];
-            const uint32_t w0 = (w & 1) ? v.z : v.x, w1 = (w & 1) ? v.w : v.y;
-            uint32_t h0, l0, h1, l1;
-            e4m3x2_split(bf16lo(w0) * mult, bf16hi(w0) * mult, h0, l0);
-            e4m3x2_split(bf16lo(w1) * mult, bf16hi(w1) * mult, h1, l1);
-            hi[w] = h0 | (h1 << 16);
-            lw[w] = l0 | (l1 << 16);
-          }
-          const uint32_t at = sw128_offset(h, half * 64 + c * 16);
-          *reinterpret_cast<uint4*>(qt + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(qt + 2048 + at) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
-        }
+        for (int i = 0; i < 4; ++i) split_queries(q_s + qb * ATD8_PT, h, half * 64 + i * 16, x[2 * i], x[2 * i + 1], mult);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[qb]);
         if (u + 1 < nu) {
-#pragma unroll
-          for (int k2 = 0; k2 < 8; ++k2) x[k2] = __ldg(q_row(unit0 + u + 1) + k2);
+          ++u;
+          load_q();
+          --u;
         }
       }
     }
@@ -635,60 +675,41 @@ attn_decode_fp8_kernel(const __grid_constant__ CUtensorMap tmap_k,    // k codes
 
 // Joins the parts of a (row, group) that CTA borders cut, in the order of the CTAs (deterministic): with
 // W_c = 2^(M_c - max M),  out = sum_c W_c acc_c / sum_c W_c l_c.  CTA = border; it acts if its border is the first inside
-// a (row, group).  The parts' maxima and sums come in with one round of loads (a chain of them took 5 us), then
-// thread = (head, 8 dims).
-constexpr int ATD8_MAXPARTS = 66;      // topk <= 64 slots, a border behind each, and the part before the first
-__global__ void __launch_bounds__(256) attn_decode_fp8_merge_kernel(const AttnDecodeFp8Args a, int grid) {
-  __shared__ float s_w[ATD8_MAXPARTS][16], s_sum[ATD8_MAXPARTS][16], s_inv[16];
-  const int c = blockIdx.x + 1;
+// a (row, group).  A CTA takes four heads (a whole (row, group) of 16 parts is 128 KiB, more than one SM reads in
+// 2 us), a warp a head, a lane 4 dims; four parts are in flight (sixteen, in registers, took as long).
+__global__ void __launch_bounds__(128) attn_decode_fp8_merge_kernel(const AttnDecodeFp8Args a, int grid) {
+  const int c = (blockIdx.x >> 2) + 1;
   const int at = atd8_first(a, c), unit = at / a.topk;
   const int first = unit * a.topk, end = first + a.topk;
   const int before = atd8_first(a, c - 1);
   const int t = unit / a.Hkv, g = unit - t * a.Hkv;
   const bool acts = at != first && before <= first && t < __ldg(a.q_start + a.num_seqs);
-  int n = 2;                                 // parts: of CTA c - 1, then part 0 of CTAs c ..
+  // parts: of CTA c - 1, then part 0 of the CTAs c .. that begin inside the (row, group)
+  int n = 2;
   if (acts)
     while (c + n - 1 < grid && atd8_first(a, c + n - 1) < end) ++n;
+  const int h = (blockIdx.x & 3) * 4 + (threadIdx.x >> 5), d0 = (threadIdx.x & 31) * 4;
+  const float* p0 = a.part + static_cast<long>(c - 1) * 2 * ATD8_PART;
   pdl_wait();                                // the partials of the kernel before, whose end this launch overlaps
   if (!acts) return;
-  auto part = [&](int i) {
-    return a.part + (static_cast<long>(c - 1 + i) * 2 + (i == 0 && before != first ? 1 : 0)) * ATD8_PART;
-  };
-  for (int i = threadIdx.x; i < n * 16; i += 256) {
-    s_w[i >> 4][i & 15] = part(i >> 4)[2048 + (i & 15)];
-    s_sum[i >> 4][i & 15] = part(i >> 4)[2064 + (i & 15)];
-  }
-  __syncthreads();
-  if (threadIdx.x < 16) {
-    const int h = threadIdx.x;
-    float mx = ATD8_LOW, l = 0.f;
-    for (int i = 0; i < n; ++i) mx = fmaxf(mx, s_w[i][h]);
-    for (int i = 0; i < n; ++i) {
-      const float w = exp2f(s_w[i][h] - mx);
-      s_w[i][h] = w;
-      l = fmaf(w, s_sum[i][h], l);
-    }
-    s_inv[h] = l == 0.f ? 0.f : 1.f / l;
-    if (a.lse) a.lse[static_cast<long>(t) * a.Hq + g * 16 + h] = l == 0.f ? -INFINITY : (mx + (log2f(l) - 8.f)) * 0.69314718055994531f;
-  }
-  __syncthreads();
-  const int h = threadIdx.x >> 4, d0 = (threadIdx.x & 15) * 8;
-  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  float M = ATD8_LOW, l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int i = 0; i < n; ++i) {
-    const float* p = part(i) + h * 128 + d0;
-    const float w = s_w[i][h];
-    const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + 4);
-    acc[0] = fmaf(w, x.x, acc[0]); acc[1] = fmaf(w, x.y, acc[1]); acc[2] = fmaf(w, x.z, acc[2]); acc[3] = fmaf(w, x.w, acc[3]);
-    acc[4] = fmaf(w, y.x, acc[4]); acc[5] = fmaf(w, y.y, acc[5]); acc[6] = fmaf(w, y.z, acc[6]); acc[7] = fmaf(w, y.w, acc[7]);
+    // CTA c - 1 may have begun before the (row, group): its part 1
+    const float* p = p0 + (i == 0 && before != first ? 1 : 2 * i) * ATD8_PART;
+    const float m = p[2048 + h], lw = p[2064 + h];
+    const float4 x = *reinterpret_cast<const float4*>(p + h * 128 + d0);
+    const float mx = fmaxf(M, m), al = exp2f(M - mx), w = exp2f(m - mx);
+    M = mx;
+    l = fmaf(w, lw, l * al);
+    acc.x = fmaf(w, x.x, acc.x * al); acc.y = fmaf(w, x.y, acc.y * al);
+    acc.z = fmaf(w, x.z, acc.z * al); acc.w = fmaf(w, x.w, acc.w * al);
   }
-  const float inv = s_inv[h];
-  uint4 r;
-  r.x = pack_bf16(acc[0] * inv, acc[1] * inv);
-  r.y = pack_bf16(acc[2] * inv, acc[3] * inv);
-  r.z = pack_bf16(acc[4] * inv, acc[5] * inv);
-  r.w = pack_bf16(acc[6] * inv, acc[7] * inv);
-  *reinterpret_cast<uint4*>(a.out + (static_cast<long>(t) * a.Hq + g * 16 + h) * 128 + d0) = r;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const long o = static_cast<long>(t) * a.Hq + g * 16 + h;
+  *reinterpret_cast<uint2*>(a.out + o * 128 + d0) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (a.lse && d0 == 0) a.lse[o] = l == 0.f ? -INFINITY : (M + (log2f(l) - 8.f)) * 0.69314718055994531f;
 }
 
 }  // namespace msa

@@ -905,7 +905,7 @@ msa_status_t msa_attn_decode_fp8(const msa_config_t* cfg, const msa_batch_t* bat
   CUDA_TRY(set_smem(msa::attn_decode_fp8_kernel, msa::ATD8_SMEM));
   msa::attn_decode_fp8_kernel<<<grid, msa::ATD8_THREADS, msa::ATD8_SMEM, stream>>>(tk, tv, a);
   if ((st = launched()) != MSA_OK || grid == 1) return st;
-  CUDA_TRY(launch_overlapped(msa::attn_decode_fp8_merge_kernel, grid - 1, 256, 0, stream, a, grid));
+  CUDA_TRY(launch_overlapped(msa::attn_decode_fp8_merge_kernel, 4 * (grid - 1), 128, 0, stream, a, grid));
   return MSA_OK;
 }
 
