@@ -280,17 +280,40 @@ def qknorm_rope_insert(cfg: Config, batch: Batch, q, k_new, v_new, q_norm_w, k_n
 
 
 def _pointers(*arrays):
-    """Device pointers of (tensor, dtype, shape, name) arguments; a None tensor is 0.  The shapes are checked first,
-    then what _need checks, and that every tensor is on the current device."""
+    """Device pointers of (tensor, dtype, shape, name) arguments; a None tensor is 0.  Every tensor must have its shape,
+    be on the current device and pass _need.  One pass over the arguments; what is wrong is found again by _refuse."""
+    here = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+    out = []
+    for t, dtype, shape, _ in arrays:
+        if t is None:
+            out.append(0)
+            continue
+        if t.get_device() != here or t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
+            _refuse(arrays, here)
+        out.append(t.data_ptr())
+    return out
+
+
+def _refuse(arrays, here: int) -> None:
+    """Raise for the first argument that _pointers does not take: shapes first, then the rest."""
     for t, _, shape, what in arrays:
         if t is not None and t.shape != shape:
             raise MsaError(MSA_ERR_INVALID_ARG, f"{what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    out = [_need(t, dtype, what) for t, dtype, _, what in arrays]
-    here = torch.cuda.current_device()
-    for t, _, _, what in arrays:
+    for t, dtype, _, what in arrays:
+        _need(t, dtype, what)
         if t is not None and t.get_device() != here:
             raise MsaError(MSA_ERR_INVALID_ARG, f"{what} is on device {t.get_device()}, but device {here} is current")
-    return out
+
+
+def _stream_here(stream) -> int:
+    """_stream for the calls that have checked their tensors to be on the current device (a third of its time)."""
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if stream is None else _stream(stream)
+
+
+def _batch_arrays(batch: Batch):
+    n, i32 = batch.num_seqs, torch.int32
+    return ((batch.q_start, i32, (n + 1,), "q_start"), (batch.ctx_len, i32, (n,), "ctx_len"),
+            (batch.page_table, i32, (n, batch.max_blocks_per_seq), "page_table"))
 
 
 def _fp8_cache(cfg: Config, batch: Batch, k_cache, v_cache, k_scale, v_scale):
@@ -317,8 +340,8 @@ def _attn_fp8(fn, cfg, batch, q, k_cache, v_cache, k_scale, v_scale, block_idx, 
     ptrs = _pointers((q, bf16, heads, "q"), *_fp8_cache(cfg, batch, k_cache, v_cache, k_scale, v_scale),
                      (block_idx, torch.int32, (batch.total_q, cfg.num_kv_heads, cfg.topk), "block_idx"),
                      (out, bf16, heads, "out"), (lse, torch.float32, rows, "lse"),
-                     (workspace, torch.uint8, (nbytes,), "workspace"))
-    _check(fn(ctypes.byref(cfg._c()), ctypes.byref(batch._c()), *ptrs, nbytes, _stream(stream)))
+                     (workspace, torch.uint8, (nbytes,), "workspace"), *_batch_arrays(batch))
+    _check(fn(cfg._c(), batch._c(host_only=True), *ptrs[:9], nbytes, _stream_here(stream)))
 
 
 def attn_decode_fp8(cfg: Config, batch: Batch, q, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale, block_idx, out, lse=None,
@@ -344,9 +367,9 @@ def qknorm_rope_insert_fp8(cfg: Config, batch: Batch, q, k_new, v_new, q_norm_w,
     bf16, heads, new = torch.bfloat16, (batch.total_q, cfg.num_q_heads, cfg.head_dim), (batch.total_q, cfg.num_kv_heads, cfg.head_dim)
     ptrs = _pointers((q, bf16, heads, "q"), (k_new, bf16, new, "k_new"), (v_new, bf16, new, "v_new"),
                      (q_norm_w, bf16, new[2:], "q_norm_w"), (k_norm_w, bf16, new[2:], "k_norm_w"), (q_out, bf16, heads, "q_out"),
-                     *_fp8_cache(cfg, batch, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale))
-    _check(load_library().msa_qknorm_rope_insert_fp8(ctypes.byref(cfg._c()), ctypes.byref(batch._c()), *ptrs, int(rotary_dim),
-                                                     float(rope_theta), float(eps), _stream(stream)))
+                     *_fp8_cache(cfg, batch, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale), *_batch_arrays(batch))
+    _check(load_library().msa_qknorm_rope_insert_fp8(cfg._c(), batch._c(host_only=True), *ptrs[:10], int(rotary_dim),
+                                                     float(rope_theta), float(eps), _stream_here(stream)))
 
 
 def advance_batch(delta, ctx_len, page_table, free_ring, pool, ctx_len_out, pool_out, q_start, slot_map=None,
@@ -366,7 +389,7 @@ def advance_batch(delta, ctx_len, page_table, free_ring, pool, ctx_len_out, pool
                      (slot_map, i32, (rows,), "slot_map"))
     if rows == 0:
         ptrs[8] = 0                    # an empty slot map is none
-    _check(load_library().msa_advance_batch(n, width, pages, int(block_size), *ptrs, rows, _stream(stream)))
+    _check(load_library().msa_advance_batch(n, width, pages, int(block_size), *ptrs, rows, _stream_here(stream)))
 
 
 def merge_partials(outs, lses, out, lse=None, stream=None) -> None:
