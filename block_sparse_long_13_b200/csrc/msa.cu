@@ -14,8 +14,8 @@
 #include "advance_batch.cuh"
 #include "attn_decode.cuh"
 #include "attn_decode_fp8.cuh"
-#include "attn_fp8.cuh"
 #include "attn_prefill.cuh"
+#include "attn_prefill_fp8.cuh"
 #include "common.cuh"
 #include "index_decode.cuh"
 #include "index_decode_tc.cuh"
@@ -794,33 +794,6 @@ msa_status_t check_attn_fp8(const msa_config_t* cfg, const msa_batch_t* batch, c
   return MSA_OK;
 }
 
-msa_status_t run_attn_fp8(const msa_config_t* cfg, const msa_batch_t* batch, const void* q, const void* k, const void* v,
-                          const float* k_scale, const float* v_scale, const int32_t* block_idx, void* out, float* lse,
-                          cudaStream_t stream) {
-  msa::AttnFp8Args a{};
-  a.q = static_cast<const __nv_bfloat16*>(q);
-  a.k_cache = static_cast<const uint8_t*>(k);
-  a.v_cache = static_cast<const uint8_t*>(v);
-  a.k_scale = k_scale;
-  a.v_scale = v_scale;
-  a.block_idx = block_idx;
-  a.out = static_cast<__nv_bfloat16*>(out);
-  a.lse = lse;
-  a.q_start = batch->q_start;
-  a.ctx_len = batch->ctx_len;
-  a.page_table = batch->page_table;
-  a.num_seqs = batch->num_seqs;
-  a.total_q = batch->total_q;
-  a.Hq = cfg->num_q_heads;
-  a.Hkv = cfg->num_kv_heads;
-  a.topk = cfg->topk;
-  a.max_blocks = batch->max_blocks_per_seq;
-  a.num_pages = batch->num_pages;
-  a.scale_log2 = softmax_scale(cfg) * 1.4426950408889634f;
-  msa::attn_fp8_plain_kernel<<<static_cast<unsigned>(batch->total_q) * cfg->num_kv_heads, 128, 0, stream>>>(a);
-  return launched();
-}
-
 // A launch that may begin while the kernel before it in the stream still runs (which lets it, and for whose end the
 // launched kernel waits on the device).
 template <typename... P, typename... A>
@@ -864,8 +837,7 @@ size_t msa_decode_fp8_workspace_bytes(const msa_config_t* cfg, const msa_batch_t
 }
 
 size_t msa_prefill_fp8_workspace_bytes(const msa_config_t* cfg, const msa_batch_t* batch) {
-  if (check_config(cfg) != MSA_OK || check_batch(batch) != MSA_OK) return 0;
-  return 256;
+  return msa_prefill_workspace_bytes(cfg, batch);   // the same schedule and partials
 }
 
 msa_status_t msa_attn_decode_fp8(const msa_config_t* cfg, const msa_batch_t* batch, const void* q,
@@ -915,8 +887,91 @@ msa_status_t msa_attn_prefill_fp8(const msa_config_t* cfg, const msa_batch_t* ba
                                   size_t workspace_bytes, cudaStream_t stream) {
   msa_status_t st = check_attn_fp8(cfg, batch, q, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale, block_idx, out, lse,
                                    workspace, workspace_bytes, msa_prefill_fp8_workspace_bytes(cfg, batch));
-  if (st != MSA_OK || batch->total_q == 0) return st;
-  return run_attn_fp8(cfg, batch, q, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale, block_idx, out, lse, stream);
+  if (st != MSA_OK) return st;
+  const PrefillWs w = prefill_plan(cfg, batch);
+  CHECK_SUP(w.nbuckets < (1L << 31) && w.max_tiles < (1L << 31), "too many (sequence, group, block) buckets");
+  if (batch->total_q == 0) return MSA_OK;
+  char* ws = static_cast<char*>(workspace);
+  const int Hq = cfg->num_q_heads, Hkv = cfg->num_kv_heads, k = cfg->topk;
+  msa::SchedFp8Args s{};
+  s.block_idx = block_idx;
+  s.q_start = batch->q_start;
+  s.ctx_len = batch->ctx_len;
+  s.page_table = batch->page_table;
+  s.k_scale = k_scale;
+  s.v_scale = v_scale;
+  s.counts = reinterpret_cast<int*>(ws + w.counts);
+  s.offsets = reinterpret_cast<int*>(ws + w.offsets);
+  s.tile_offsets = reinterpret_cast<int*>(ws + w.tile_offsets);
+  s.cursor = reinterpret_cast<int*>(ws + w.cursor);
+  s.entries = reinterpret_cast<int*>(ws + w.entries);
+  s.total_tiles = reinterpret_cast<int*>(ws + w.total_tiles);
+  s.tile_rec = reinterpret_cast<int4*>(ws + w.tile_rec);
+  s.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
+  s.num_seqs = batch->num_seqs;
+  s.total_q = batch->total_q;
+  s.Hq = Hq;
+  s.Hkv = Hkv;
+  s.topk = k;
+  s.max_blocks = batch->max_blocks_per_seq;
+  s.nbuckets = static_cast<int>(w.nbuckets);
+  s.num_pages = batch->num_pages;
+  s.max_tiles = static_cast<int>(w.max_tiles);
+  msa::SchedArgs scan{};
+  scan.counts = s.counts;
+  scan.offsets = s.offsets;
+  scan.tile_offsets = s.tile_offsets;
+  scan.cursor = s.cursor;
+  scan.total_tiles = s.total_tiles;
+  scan.nbuckets = s.nbuckets;
+  CUDA_TRY(cudaMemsetAsync(s.counts, 0, w.nbuckets * 4, stream));
+  const unsigned sgrid = static_cast<unsigned>((batch->total_q + msa::SCHED_ROWS - 1) / msa::SCHED_ROWS);
+  msa::sched_fp8_kernel<<<sgrid, 256, 0, stream>>>(s, 0);
+  if ((st = launched()) != MSA_OK) return st;
+  msa::sched_scan_kernel<<<1, 1024, 0, stream>>>(scan);
+  if ((st = launched()) != MSA_OK) return st;
+  msa::sched_fp8_kernel<<<sgrid, 256, 0, stream>>>(s, 1);
+  if ((st = launched()) != MSA_OK) return st;
+  const int sms = num_sms();
+  const long tgrid = std::min<long>((w.max_tiles + 255) / 256, 8L * sms);
+  msa::sched_fp8_tiles_kernel<<<static_cast<unsigned>(std::max<long>(1, tgrid)), 256, 0, stream>>>(s);
+  if ((st = launched()) != MSA_OK) return st;
+
+  CUtensorMap tq, tpo;
+  {
+    const uint64_t dims[2] = {128, static_cast<uint64_t>(batch->total_q) * Hq};
+    const uint64_t dims_po[2] = {128, static_cast<uint64_t>(batch->total_q) * k * Hq};
+    const uint64_t strides[1] = {256};
+    const uint32_t box[2] = {64, 16};
+    if ((st = make_map(&tq, q, 2, dims, strides, box)) != MSA_OK) return st;
+    if ((st = make_map(&tpo, ws + w.part_o, 2, dims_po, strides, box)) != MSA_OK) return st;
+  }
+  msa::AttnPrefillFp8Args a{};
+  a.tile_rec = s.tile_rec;
+  a.total_tiles = s.total_tiles;
+  a.k_cache = static_cast<const uint8_t*>(k_cache_e4m3);
+  a.v_cache = static_cast<const uint8_t*>(v_cache_e4m3);
+  a.part_lse = s.part_lse;
+  a.Hq = Hq;
+  a.topk = k;
+  a.max_tiles = s.max_tiles;
+  a.scale_log2 = softmax_scale(cfg) * 1.4426950408889634f;
+  CUDA_TRY(set_smem(msa::attn_prefill_fp8_kernel, msa::ATTP_SMEM));
+  msa::attn_prefill_fp8_kernel<<<sms, msa::ATP8_THREADS, msa::ATTP_SMEM, stream>>>(tq, tpo, a);
+  if ((st = launched()) != MSA_OK) return st;
+  msa::MergeFp8Args m{};
+  m.part_o = reinterpret_cast<const __nv_bfloat16*>(ws + w.part_o);
+  m.part_lse = s.part_lse;
+  m.block_idx = block_idx;
+  m.q_start = batch->q_start;
+  m.out = static_cast<__nv_bfloat16*>(out);
+  m.lse = lse;
+  m.num_seqs = batch->num_seqs;
+  m.Hq = Hq;
+  m.Hkv = Hkv;
+  m.topk = k;
+  msa::attn_merge_fp8_kernel<<<static_cast<unsigned>(batch->total_q) * Hkv, 256, 0, stream>>>(m);
+  return launched();
 }
 
 msa_status_t msa_qknorm_rope_insert_fp8(const msa_config_t* cfg, const msa_batch_t* batch, const void* q,
