@@ -4,10 +4,12 @@
 // The block-major form of attn_prefill.cuh (a tile stacks the 16 heads of up to 8 tokens that selected the block;
 // S = Q K^T and O = P V on tcgen05; per-slot partials; log-sum-exp merge), over codes:
 //   x_j = (scale log2 e) ks_b (q . ck_j),   O_b = vs_b sum_j 2^(x_j - m) cv_j / l,   lse_b = (m + log2 l) ln 2.
-// The codes are widened to bf16, which holds every e4m3 value, once per (tile run, block) by four converter warps, and
-// the scales stay fp32 factors of the softmax and of the output: nothing is rounded that the bf16 form does not round.
+// The codes are widened once per (run of tiles, block) by four converter warps, K to bf16 (an MMA's operands have one
+// type, and the queries are bf16) and V to f16 (one conversion instruction for two codes; P is then f16 too, three bits
+// more than bf16 for numbers of at most 1); both hold every e4m3 value.  The scales stay fp32 factors of the softmax
+// and of the output: nothing is rounded that the bf16 form does not round.
 // Feeding the tensor cores with the codes, as the decode form does, would take P in two 8-bit parts, 256 more
-// instructions for each row of 128 keys in the softmax warps that set this kernel's pace; a block's widening is 48
+// instructions for each row of 128 keys in the softmax warps that set this kernel's pace; a block's widening is 20 to 45
 // instructions per 16 codes, once for all tokens that selected it, in warps of their own.
 #pragma once
 #include "attn_prefill.cuh"
@@ -31,6 +33,13 @@ __device__ __forceinline__ uint4 without_nan(uint4 x) {   // NaN codes become 0
   auto clear = [](uint32_t w) { const uint32_t b = nan_bytes(w) >> 7; return w & ~(b * 0xFFu); };
   return make_uint4(clear(x.x), clear(x.y), clear(x.z), clear(x.w));
 }
+// whether there is one among the codes of a warp
+__device__ __forceinline__ bool warp_has_nan(const uint4 (&x)[8]) {
+  uint32_t any = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) any |= nan_bytes(x[k].x) | nan_bytes(x[k].y) | nan_bytes(x[k].z) | nan_bytes(x[k].w);
+  return __any_sync(0xFFFFFFFFu, any != 0u);
+}
 // Two codes (bytes 1 and 3 of t) as bf16: exponent and mantissa move to bits 10..4, where they stand for the code's
 // value times 2^-120 (bias 127 instead of 7; subnormals too), and a product with 2^120 is exact.
 __device__ __forceinline__ uint32_t widen2(uint32_t t) {
@@ -39,22 +48,9 @@ __device__ __forceinline__ uint32_t widen2(uint32_t t) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(y), "r"(0x7B807B80u));
   return r;
 }
-// piece c (16 codes: key c / 8, dims 16 (c % 8) ..) of a block to its place in the bf16 tile [half][128 keys][64 dims]
-__device__ __forceinline__ void widen16(uint8_t* tile, int c, const uint4& x) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  uint32_t y[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    y[2 * i] = widen2(__byte_perm(w[i], 0, 0x1404));       // codes 0 and 1
-    y[2 * i + 1] = widen2(__byte_perm(w[i], 0, 0x3424));   // codes 2 and 3
-  }
-  if (has_nan(x)) {                                        // the moved bits of a NaN code are 480: make them NaN
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if ((y[i] & 0x7FFFu) == 0x43F0u) y[i] |= 0x7FC0u;
-      if ((y[i] & 0x7FFF0000u) == 0x43F00000u) y[i] |= 0x7FC00000u;
-    }
-  }
+// the 16 values of piece c (key c / 8, dims 16 (c % 8) ..) of a block to their place in the 16-bit tile
+// [half][128 keys][64 dims]
+__device__ __forceinline__ void store16(uint8_t* tile, int c, const uint32_t (&y)[8]) {
   const int key = c >> 3, d = (c & 7) * 16;
   uint8_t* base = tile + (d >> 6) * 16384;
   const uint32_t at0 = sw128_offset(key, (d & 63) * 2), at1 = sw128_offset(key, (d & 63) * 2 + 16);
@@ -63,6 +59,44 @@ __device__ __forceinline__ void widen16(uint8_t* tile, int c, const uint4& x) {
   const bool swap = d >= 64;
   *reinterpret_cast<uint4*>(base + (swap ? at1 : at0)) = swap ? hi : lo;
   *reinterpret_cast<uint4*>(base + (swap ? at0 : at1)) = swap ? lo : hi;
+}
+template <bool NANS>
+__device__ __forceinline__ void widen16_bf16(uint8_t* tile, int c, const uint4& x) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t y[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    y[2 * i] = widen2(__byte_perm(w[i], 0, 0x1404));       // codes 0 and 1
+    y[2 * i + 1] = widen2(__byte_perm(w[i], 0, 0x3424));   // codes 2 and 3
+  }
+  if (NANS) {                                              // the moved bits of a NaN code are 480: make them NaN
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if ((y[i] & 0x7FFFu) == 0x43F0u) y[i] |= 0x7FC0u;
+      if ((y[i] & 0x7FFF0000u) == 0x43F00000u) y[i] |= 0x7FC00000u;
+    }
+  }
+  store16(tile, c, y);
+}
+__device__ __forceinline__ void widen16_f16(uint8_t* tile, int c, const uint4& x) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  uint32_t y[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y[2 * i]) : "h"(static_cast<uint16_t>(w[i] & 0xFFFFu)));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y[2 * i + 1]) : "h"(static_cast<uint16_t>(w[i] >> 16)));
+  }
+  store16(tile, c, y);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Instruction descriptor, kind::f16: f16 x f16 -> fp32
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
 }
 
 // ------------------------------------------------------------------ schedule
@@ -340,7 +374,7 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
     // This one thread's instruction latency is on the critical path: descriptors are built once
     // (only the 14-bit start address, in 16-byte units, moves) and ring positions are counters.
     const uint32_t id_s = idesc_bf16(128, 128, false, false);
-    const uint32_t id_pv = idesc_bf16(128, 128, false, true);
+    const uint32_t id_pv = idesc_f16(128, 128, true);
     const uint64_t qdesc0 = sdesc_sw128(smem_u32(q_s), 16, 1024);
     const uint64_t kdesc0 = sdesc_sw128(smem_u32(k_s), 16, 1024);
     const uint64_t vdesc0 = sdesc_sw128(smem_u32(v_s), 16384, 1024);
@@ -408,7 +442,7 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
   }
   } else if (warp < 8) {
     regs_dec<ATP8_REGS_CONV>();
-    // ------------------------------------------------------------ converters: a bucket's codes to bf16
+    // ------------------------------------------------------------ converters: a bucket's codes to 16 bits
     // A thread takes every 128th 16-byte piece of the tile.  K waits for the previous bucket's last S only and V for its
     // last P V, and the next bucket's K codes are in registers by then, so a change of bucket costs the tensor
     // cores one conversion of K.
@@ -416,70 +450,89 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
     int4 ra = make_int4(-1, 0, 0, 0), rb = ra;               // records of tiles (batch + lane)
     int i = 0, cur = -1, row = 0, valid = 0;
     auto next_bucket = [&]() -> bool {                       // to the next bucket of this CTA's tiles; uniform
-      for (; i < ntile; ++i) {
-        if ((i & 31) == 0) {
-          ra.x = cur;
-          if (i + lane < ntile) {
-            const int4* p = a.tile_rec + static_cast<long>(tile_of(i + lane)) * 4;
-            ra = __ldg(p);
-            rb = __ldg(p + 1);
-          }
+      while (i < ntile) {
+        const int at = i & 31;
+        if (at == 0 && i + lane < ntile) {
+          const int4* p = a.tile_rec + static_cast<long>(tile_of(i + lane)) * 4;
+          ra = __ldg(p);
+          rb = __ldg(p + 1);
         }
-        const int bucket = __shfl_sync(0xFFFFFFFFu, ra.x, i & 31);
-        if (bucket != cur) {
-          cur = bucket;
-          row = __shfl_sync(0xFFFFFFFFu, ra.y, i & 31);
-          valid = __shfl_sync(0xFFFFFFFFu, rb.y, i & 31) >> 8;
-          ++i;
+        // lanes of this batch's tiles from i on whose bucket is another one
+        const uint32_t others = __ballot_sync(0xFFFFFFFFu, ra.x != cur && i - at + lane < ntile) & (0xFFFFFFFFu << at);
+        if (others) {
+          const int src = __ffs(others) - 1;
+          cur = __shfl_sync(0xFFFFFFFFu, ra.x, src);
+          row = __shfl_sync(0xFFFFFFFFu, ra.y, src);
+          valid = __shfl_sync(0xFFFFFFFFu, rb.y, src) >> 8;
+          i += src - at + 1;
           return true;
         }
+        i += 32 - at;
       }
       return false;
     };
     uint4 x[8];
+    auto codes = [&](const uint8_t* cache) { return reinterpret_cast<const uint4*>(cache + static_cast<long>(row) * 128) + ct; };
     auto load = [&](const uint8_t* cache) {
-      const uint4* p = reinterpret_cast<const uint4*>(cache + static_cast<long>(row) * 128) + ct;
+      const uint4* p = codes(cache);
 #pragma unroll
       for (int k = 0; k < 8; ++k) x[k] = __ldg(p + k * 128);
     };
+    // V comes by way of L2: it is wanted soon after K, and from DRAM, beside the partials' stores, a change of bucket
+    // waited up to 12 us for it (2.17 ms a 128K chunk instead of TIMEV).
+    auto prefetch_v = [&]() {
+      asm volatile("prefetch.global.L2::evict_last [%0];" ::"l"(a.v_cache + (static_cast<long>(row) + ct) * 128));
+    };
     bool have = next_bucket(), ok = true;
-    if (have) load(a.k_cache);
+    if (have) {
+      load(a.k_cache);
+      prefetch_v();
+    }
     for (uint32_t it = 0; have && ok; ++it) {
       ok = mbar_wait_warp(&k_empty, (it & 1) ^ 1, &s_abort);
       if (!ok) break;
+      if (warp_has_nan(x)) {                     // rare: piece by piece, out of L2 again
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) widen16_bf16<true>(k_s, k * 128 + ct, __ldg(codes(a.k_cache) + k * 128));
+      } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        widen16(k_s, k * 128 + ct, x[k]);
-        asm volatile("" ::: "memory");              // one piece after the other: fewer registers
+        for (int k = 0; k < 8; ++k) widen16_bf16<false>(k_s, k * 128 + ct, x[k]);
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&k_full);
       load(a.v_cache);
-      const int rows = valid;
-      have = next_bucket();
       ok = mbar_wait_warp(&v_empty, (it & 1) ^ 1, &s_abort);
       if (!ok) break;
       int bad = 128;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int key = (k * 128 + ct) >> 3;
+      if (valid < 128 || warp_has_nan(x)) {
         // slots behind the sequence hold anything; a NaN that counts is noted and taken out (0 x NaN is NaN for the
         // rows that do not see it)
-        if (key >= rows) x[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (has_nan(x[k])) {
-          bad = min(bad, key);
-          x[k] = without_nan(x[k]);
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) {
+          const int key = (k * 128 + ct) >> 3;
+          uint4 y = make_uint4(0u, 0u, 0u, 0u);
+          if (key < valid) y = __ldg(codes(a.v_cache) + k * 128);
+          if (has_nan(y)) {
+            bad = min(bad, key);
+            y = without_nan(y);
+          }
+          widen16_f16(v_s, k * 128 + ct, y);
         }
-        widen16(v_s, k * 128 + ct, x[k]);
-        asm volatile("" ::: "memory");
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) widen16_f16(v_s, k * 128 + ct, x[k]);
       }
       bad = __reduce_min_sync(0xFFFFFFFFu, bad);
       if (lane == 0) s_vnan[it & 3][warp - 4] = bad;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&v_full);
-      if (have) load(a.k_cache);
+      have = next_bucket();
+      if (have) {
+        load(a.k_cache);
+        prefetch_v();
+      }
     }
   } else {
     regs_inc<ATP8_REGS_SOFTMAX>();
@@ -558,7 +611,7 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
       for (int c = 0; c < 32; ++c) mx[c & 7] = fmax3(mx[c & 7], fmaxf(v0[c], v1[c]), fmaxf(v2[c], v3[c]));
       const float m = fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], fmax3(mx[4], mx[5], mx[6]), mx[7]));
       const float mc = (m > -INFINITY) ? m * sc : 0.f;   // -inf only on rows past the tile's entries
-      // ---- P = exp2(scale * S - max) as bf16 pairs into P[w] (TMEM), two halves of 64 keys
+      // ---- P = exp2(scale * S - max) as f16 pairs into P[w] (TMEM), two halves of 64 keys
       float l0 = 0.f, l1 = 0.f;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -570,7 +623,7 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
           const float x1 = c + 1 < 32 ? v0[c + 1] : c + 1 < 64 ? v1[c - 31] : c + 1 < 96 ? v2[c - 63] : v3[c - 95];
           const float p0 = exp2f(fmaf(x0, sc, -mc)), p1 = exp2f(fmaf(x1, sc, -mc));   // exp2(-inf) = 0
           if (q2 & 1) l1 += p0 + p1; else l0 += p0 + p1;
-          pk[q2] = pack_bf16(p0, p1);
+          pk[q2] = pack_f16(p0, p1);
         }
         tmem_st32(lane_addr + ATTP_TM_S + w * 128 + half * 32, pk);   // S columns already in registers
       }

@@ -116,6 +116,8 @@ SHAPES = {
     "sequences without rows": dict(ctx=[400, 500, 300, 50, 600], nq=[0, 2, 0, 1, 0], extra_width=3),
     "rows of one sequence": dict(ctx=[1500], nq=[150], kv=2, topk=4),
     "more rows than one wave": dict(ctx=[300] * 60, nq=[3] * 60, topk=3),
+    "many tiles a block": dict(ctx=[1700, 300], nq=[1600, 260], kv=1, topk=4),
+    "blocks shared by few rows": dict(ctx=[6000, 3000], nq=[300, 200], kv=2, topk=16),
 }
 
 
@@ -125,7 +127,7 @@ def test_attention_matches_oracle(cuda_ok, shape, which):
     c = Case(3, **SHAPES[shape])
     out, lse = c.run(which)
     assert msa.device_status() == msa.MSA_OK
-    c.check(out, lse)
+    c.check(out, lse, range(0, c.rows, max(1, c.rows // 200)))
 
 
 @pytest.mark.parametrize("which", ["decode", "prefill"])
