@@ -38,6 +38,7 @@
 #pragma once
 #include "attn_decode.cuh"
 #include "e4m3.cuh"
+#include "launch_order.cuh"
 
 namespace msa {
 
@@ -128,9 +129,6 @@ __device__ __forceinline__ void e4m3x2_split(float a, float b, uint32_t& hi, uin
   hi = u;
   lo = v;
 }
-
-__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // A head's queries come to (224, 448] times 2^k, 448 = 1.75 * 2^8, by the largest of them (|q| as bf16 bits: NaN above
 // infinity above the rest).

@@ -17,19 +17,24 @@
 // once.  The pieces are the first block of each sequence (CTA = sequence) and the blocks that begin inside
 // the call's rows (CTA = window of 128 rows, which holds one such block for each sequence that crosses a
 // block border in it): num_seqs + total_q / 128 CTAs a head, no search by the host.
-// q_norm_rope_kernel: one CTA a row, in and out by bulk copies.
+// At most 148 CTAs walk the pieces, so that all of them run from the start and q_norm_rope_kernel, which needs nothing
+// from them, may be launched beside them (an ordinary launch after them: 166 us for 16,384 rows, 83 and 86 for the two).
+// q_norm_rope_kernel: one CTA a row, in and out by bulk copies; bound by HBM (6.2 TB/s).
 //
 // Angles: p * theta^(-2i/r) is taken in turns, in double, from a table that the host fills (theta^(-2i/r) / 2 pi):
 // the fraction of a turn is exact to 2^-31 at positions up to 2^22, and cospi / sinpi of it in fp32 lose
 // nothing further, where a double sincos would cost some hundred double instructions a pair.
 #pragma once
 #include "e4m3.cuh"
+#include "launch_order.cuh"
 #include "qk_rope_insert.cuh"
 
 namespace msa {
 
-constexpr int KVI_THREADS = 256;                       // 16 half-warps, a row's head each
-constexpr int KVI_ITERS = 128 / (KVI_THREADS / 16);    // rows of a full page per half-warp
+constexpr int KVI_THREADS = 512;                       // 32 half-warps, a row's head each
+constexpr int KVI_ROWS = KVI_THREADS / 16;             // rows at a time
+constexpr int KVI_ITERS = 128 / KVI_ROWS;              // rows of a full page per half-warp
+constexpr int KVI_GRID = 148;                          // CTAs at most
 
 struct RopeTable { double turns[QKR_D / 2]; };         // theta^(-2i/r) / (2 pi), i < rotary_dim / 2
 
@@ -44,7 +49,7 @@ struct KvInsertArgs {
   const int32_t* q_start;
   const int32_t* ctx_len;
   const int32_t* page_table;
-  int num_seqs, total_q, Hkv, max_blocks, num_pages, rotary_dim;
+  int num_seqs, total_q, Hkv, max_blocks, num_pages, rotary_dim, pieces;
   float eps;
 };
 
@@ -95,7 +100,7 @@ __device__ __forceinline__ void kv_insert_piece(const KvInsertArgs& a, const Rop
   uint4 vv[KVI_ITERS];
 #pragma unroll
   for (int it = 0; it < KVI_ITERS; ++it) {
-    const int r = it * 16 + row0;
+    const int r = it * KVI_ROWS + row0;
     ka[it] = kb[it] = make_uint2(0u, 0u);
     vv[it] = make_uint4(0u, 0u, 0u, 0u);
     if (r < n) {
@@ -116,7 +121,7 @@ __device__ __forceinline__ void kv_insert_piece(const KvInsertArgs& a, const Rop
   float kmax = 0.f, vmax = 0.f;
 #pragma unroll
   for (int it = 0; it < KVI_ITERS; ++it) {
-    if (it * 16 >= n) break;                             // uniform
+    if (it * KVI_ROWS >= n) break;                             // uniform
     float xa[4] = {bf16lo(ka[it].x), bf16hi(ka[it].x), bf16lo(ka[it].y), bf16hi(ka[it].y)};
     float xb[4] = {bf16lo(kb[it].x), bf16hi(kb[it].x), bf16lo(kb[it].y), bf16hi(kb[it].y)};
     float ss = 0.f;
@@ -125,7 +130,7 @@ __device__ __forceinline__ void kv_insert_piece(const KvInsertArgs& a, const Rop
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
     const float inv = rsqrtf(ss * (1.f / QKR_D) + a.eps);
-    const int p = p0 + it * 16 + row0;
+    const int p = p0 + it * KVI_ROWS + row0;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const float ya = xa[u] * inv * wa[u], yb = xb[u] * inv * wb[u];
@@ -134,7 +139,7 @@ __device__ __forceinline__ void kv_insert_piece(const KvInsertArgs& a, const Rop
       ky[it][u] = rot ? ya * cs - yb * sn : ya;
       ky[it][4 + u] = rot ? yb * cs + ya * sn : yb;
     }
-    if (it * 16 + row0 < n) {                            // rows past the piece hold nothing
+    if (it * KVI_ROWS + row0 < n) {                            // rows past the piece hold nothing
 #pragma unroll
       for (int u = 0; u < 8; ++u) kmax = fmaxf(kmax, finite_abs(ky[it][u]));
       const uint32_t* w = reinterpret_cast<const uint32_t*>(&vv[it]);
@@ -158,21 +163,28 @@ __device__ __forceinline__ void kv_insert_piece(const KvInsertArgs& a, const Rop
   const bool k_grown = slot0 == 0 || !(k_old > 0.f) || kmax > E4M3_MAX * k_old;
   const bool v_grown = slot0 == 0 || !(v_old > 0.f) || vmax > E4M3_MAX * v_old;
   const float ks = k_grown ? e4m3_block_scale(kmax) : k_old, vs = v_grown ? e4m3_block_scale(vmax) : v_old;
+  // a power of two's reciprocal is exact, and so is a product with it; other scales (a cache that something else wrote)
+  // are divided by
+  const bool exact = (((__float_as_uint(ks) | __float_as_uint(vs)) & 0x7FFFFFu) == 0u) && ks >= 0x1p-126f && vs >= 0x1p-126f;
+  const float ki = __uint_as_float(0x7F000000u - __float_as_uint(ks)), vi = __uint_as_float(0x7F000000u - __float_as_uint(vs));
   uint8_t* kt = a.k_cache + tile * (128 * QKR_D);
   uint8_t* vt = a.v_cache + tile * (128 * QKR_D);
 #pragma unroll
   for (int it = 0; it < KVI_ITERS; ++it) {
-    const int r = it * 16 + row0;
+    const int r = it * KVI_ROWS + row0;
     if (r >= n) break;
     uint8_t* kr = kt + (slot0 + r) * QKR_D;
     float z[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) z[u] = __fdiv_rn(ky[it][u], ks);
+    for (int u = 0; u < 8; ++u) z[u] = exact ? ky[it][u] * ki : __fdiv_rn(ky[it][u], ks);
     *reinterpret_cast<uint32_t*>(kr + ca) = e4m3x4_of(z[0], z[1], z[2], z[3]);
     *reinterpret_cast<uint32_t*>(kr + cb) = e4m3x4_of(z[4], z[5], z[6], z[7]);
     const uint32_t* w = reinterpret_cast<const uint32_t*>(&vv[it]);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) { z[2 * u] = __fdiv_rn(bf16lo(w[u]), vs); z[2 * u + 1] = __fdiv_rn(bf16hi(w[u]), vs); }
+    for (int u = 0; u < 4; ++u) {
+      z[2 * u] = exact ? bf16lo(w[u]) * vi : __fdiv_rn(bf16lo(w[u]), vs);
+      z[2 * u + 1] = exact ? bf16hi(w[u]) * vi : __fdiv_rn(bf16hi(w[u]), vs);
+    }
     *reinterpret_cast<uint2*>(vt + (slot0 + r) * QKR_D + 8 * hl) =
         make_uint2(e4m3x4_of(z[0], z[1], z[2], z[3]), e4m3x4_of(z[4], z[5], z[6], z[7]));
   }
@@ -184,11 +196,11 @@ __device__ __forceinline__ void kv_insert_piece(const KvInsertArgs& a, const Rop
   }
 }
 
-__global__ void __launch_bounds__(KVI_THREADS)
+__global__ void __launch_bounds__(KVI_THREADS, 1)
 kv_insert_fp8_kernel(const KvInsertArgs a, const __grid_constant__ RopeTable tab) {
   __shared__ float s_max[2][KVI_THREADS / 32];
   __shared__ int s_t[128], s_p[128], s_s[128], s_cnt[4];
-  const int g = blockIdx.x % a.Hkv, i = blockIdx.x / a.Hkv;
+  pdl_launch_dependents();                               // the queries' kernel needs nothing from this one
   // the cache page of sequence s's block b; -1 (and flagged) if there is none
   auto page_of = [&](int s, int b) -> int {
     const int page = b >= 0 && b < a.max_blocks ? __ldg(a.page_table + static_cast<long>(s) * a.max_blocks + b) : -1;
@@ -196,47 +208,52 @@ kv_insert_fp8_kernel(const KvInsertArgs a, const __grid_constant__ RopeTable tab
     if (threadIdx.x == 0) flag_error(MSA_DEV_BOUNDS);
     return -1;
   };
-  if (i < a.num_seqs) {                                  // the block that the sequence's first new row falls in
-    const int t0 = __ldg(a.q_start + i), nq = __ldg(a.q_start + i + 1) - t0, p0 = __ldg(a.ctx_len + i) - nq;
-    if (nq <= 0) return;
-    if (p0 < 0 || t0 < 0 || t0 + nq > a.total_q) {
-      if (threadIdx.x == 0) flag_error(MSA_DEV_BOUNDS);
-      return;
-    }
-    const int page = page_of(i, p0 >> 7);
-    if (page >= 0) kv_insert_piece(a, tab, t0, p0, min(nq, 128 - (p0 & 127)), page, g, s_max);
-    return;
-  }
-  // the blocks that begin at a row of this window (not their sequence's first row)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rows = min(a.total_q, __ldg(a.q_start + a.num_seqs));
-  unsigned vote = 0;
-  int t = 0, s = 0, p = 0;
-  bool lead = false;
-  if (tid < 128) {
-    t = (i - a.num_seqs) * 128 + tid;
-    if (t < rows) {
-      s = find_seq(a.q_start, a.num_seqs, t);
-      const int end = __ldg(a.q_start + s + 1);
-      p = __ldg(a.ctx_len + s) - end + t;
-      lead = t != __ldg(a.q_start + s) && p > 0 && (p & 127) == 0;
+  for (int piece = blockIdx.x; piece < a.pieces; piece += gridDim.x) {
+    const int g = piece % a.Hkv, i = piece / a.Hkv;
+    if (i < a.num_seqs) {                                // the block that the sequence's first new row falls in
+      const int t0 = __ldg(a.q_start + i), nq = __ldg(a.q_start + i + 1) - t0, p0 = __ldg(a.ctx_len + i) - nq;
+      if (nq <= 0) continue;
+      if (p0 < 0 || t0 < 0 || t0 + nq > a.total_q) {
+        if (tid == 0) flag_error(MSA_DEV_BOUNDS);
+        continue;
+      }
+      const int page = page_of(i, p0 >> 7);
+      if (page >= 0) kv_insert_piece(a, tab, t0, p0, min(nq, 128 - (p0 & 127)), page, g, s_max);
+      __syncthreads();                                   // s_max is written again
+      continue;
     }
-    vote = __ballot_sync(0xFFFFFFFFu, lead);
-    if (lane == 0) s_cnt[warp] = __popc(vote);
-  }
-  __syncthreads();
-  if (lead) {
-    int at = __popc(vote & ((1u << lane) - 1u));
-    for (int w = 0; w < warp; ++w) at += s_cnt[w];
-    s_t[at] = t; s_p[at] = p; s_s[at] = s;
-  }
-  __syncthreads();
-  const int n_lead = s_cnt[0] + s_cnt[1] + s_cnt[2] + s_cnt[3];
-  for (int j = 0; j < n_lead; ++j) {
-    const int page = page_of(s_s[j], s_p[j] >> 7);
-    if (page >= 0)
-      kv_insert_piece(a, tab, s_t[j], s_p[j], min(128, min(rows, __ldg(a.q_start + s_s[j] + 1)) - s_t[j]), page, g, s_max);
-    __syncthreads();                                     // s_max is written again
+    // the blocks that begin at a row of this window (not their sequence's first row)
+    unsigned vote = 0;
+    int t = 0, s = 0, p = 0;
+    bool lead = false;
+    if (tid < 128) {
+      t = (i - a.num_seqs) * 128 + tid;
+      if (t < rows) {
+        s = find_seq(a.q_start, a.num_seqs, t);
+        const int end = __ldg(a.q_start + s + 1);
+        p = __ldg(a.ctx_len + s) - end + t;
+        lead = t != __ldg(a.q_start + s) && p > 0 && (p & 127) == 0;
+      }
+      vote = __ballot_sync(0xFFFFFFFFu, lead);
+      if (lane == 0) s_cnt[warp] = __popc(vote);
+    }
+    __syncthreads();
+    if (lead) {
+      int at = __popc(vote & ((1u << lane) - 1u));
+      for (int w = 0; w < warp; ++w) at += s_cnt[w];
+      s_t[at] = t; s_p[at] = p; s_s[at] = s;
+    }
+    __syncthreads();
+    const int n_lead = s_cnt[0] + s_cnt[1] + s_cnt[2] + s_cnt[3];
+    for (int j = 0; j < n_lead; ++j) {
+      const int page = page_of(s_s[j], s_p[j] >> 7);
+      if (page >= 0)
+        kv_insert_piece(a, tab, s_t[j], s_p[j], min(128, min(rows, __ldg(a.q_start + s_s[j] + 1)) - s_t[j]), page, g, s_max);
+      __syncthreads();                                   // s_max is written again
+    }
+    __syncthreads();                                     // and so are the window's lists
   }
 }
 
@@ -280,6 +297,7 @@ q_norm_rope_kernel(const QNormRopeArgs a, const __grid_constant__ RopeTable tab)
   __syncthreads();
   if (tid == 0 && !mbar_wait(&s_bar, 0, &s_abort)) mbar_wait_drain(&s_bar, 0);
   __syncthreads();
+  if (blockIdx.x == gridDim.x - 1 && tid == 0) pdl_wait();   // this kernel ends after the one that it runs beside
   if (s_abort || padded) return;
   float cs[4], sn[4], wa[4], wb[4];
 #pragma unroll

@@ -1017,7 +1017,8 @@ msa_status_t msa_qknorm_rope_insert_fp8(const msa_config_t* cfg, const msa_batch
   a.rotary_dim = rotary_dim;
   a.eps = eps;
   const unsigned pieces = static_cast<unsigned>(batch->num_seqs) + (static_cast<unsigned>(batch->total_q) + 127u) / 128u;
-  msa::kv_insert_fp8_kernel<<<pieces * a.Hkv, msa::KVI_THREADS, 0, stream>>>(a, tab);
+  a.pieces = static_cast<int>(pieces) * a.Hkv;
+  msa::kv_insert_fp8_kernel<<<std::min(a.pieces, msa::KVI_GRID), msa::KVI_THREADS, 0, stream>>>(a, tab);
   if ((st = launched()) != MSA_OK) return st;
   msa::QNormRopeArgs qa{};
   qa.q = static_cast<const __nv_bfloat16*>(q);
@@ -1033,8 +1034,9 @@ msa_status_t msa_qknorm_rope_insert_fp8(const msa_config_t* cfg, const msa_batch
   CUDA_TRY(set_smem(msa::q_norm_rope_kernel, smem));
   CUDA_TRY(cudaFuncSetAttribute(msa::q_norm_rope_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
                                 cudaSharedmemCarveoutMaxShared));
-  msa::q_norm_rope_kernel<<<static_cast<unsigned>(batch->total_q), msa::QKR_THREADS, smem, stream>>>(qa, tab);
-  return launched();
+  CUDA_TRY(launch_overlapped(msa::q_norm_rope_kernel, static_cast<unsigned>(batch->total_q), msa::QKR_THREADS, smem, stream,
+                             qa, tab));
+  return MSA_OK;
 }
 
 msa_status_t msa_advance_batch(int32_t num_seqs, int32_t max_blocks_per_seq, int32_t num_pages, int32_t block_size,
