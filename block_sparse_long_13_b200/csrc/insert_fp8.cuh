@@ -21,9 +21,10 @@
 // from them, may be launched beside them (an ordinary launch after them: 166 us for 16,384 rows, 83 and 86 for the two).
 // q_norm_rope_kernel: one CTA a row, in and out by bulk copies; bound by HBM (6.2 TB/s).
 //
-// Angles: p * theta^(-2i/r) is taken in turns, in double, from a table that the host fills (theta^(-2i/r) / 2 pi):
-// the fraction of a turn is exact to 2^-31 at positions up to 2^22, and cospi / sinpi of it in fp32 lose
-// nothing further, where a double sincos would cost some hundred double instructions a pair.
+// Angles: theta^(-2i/r) / 2 pi turns a position, as 64-bit fractions of a turn from a table that the host fills.  Their
+// product with the position modulo 2^64 is the fraction of a turn, off by 2^-64 a position (2^-40 at 2^24), in two
+// integer multiplications where a double product and its sincos would cost some hundred double instructions; cospi and
+// sinpi of it in fp32 lose nothing further.
 #pragma once
 #include "e4m3.cuh"
 #include "launch_order.cuh"
@@ -36,7 +37,7 @@ constexpr int KVI_ROWS = KVI_THREADS / 16;             // rows at a time
 constexpr int KVI_ITERS = 128 / KVI_ROWS;              // rows of a full page per half-warp
 constexpr int KVI_GRID = 148;                          // CTAs at most
 
-struct RopeTable { double turns[QKR_D / 2]; };         // theta^(-2i/r) / (2 pi), i < rotary_dim / 2
+struct RopeTable { unsigned long long turns[QKR_D / 2]; };   // theta^(-2i/r) / (2 pi) modulo 1, times 2^64, i < rotary_dim / 2
 
 struct KvInsertArgs {
   const __nv_bfloat16* k_new;    // [total_q][Hkv][128]
@@ -53,11 +54,10 @@ struct KvInsertArgs {
   float eps;
 };
 
-// cos and sin of the angle of pair i at position p
-__device__ __forceinline__ void rope_angle(double turns, int p, float& cs, float& sn) {
-  const double a = static_cast<double>(p) * turns;
-  const float f = static_cast<float>(a - rint(a)) * 2.f;   // half turns in [-1, 1]
-  sincospif(f, &sn, &cs);
+// cos and sin of the angle of a pair at position p
+__device__ __forceinline__ void rope_angle(unsigned long long turns, int p, float& cs, float& sn) {
+  const unsigned long long a = turns * static_cast<unsigned long long>(static_cast<long long>(p));
+  sincospif(static_cast<float>(static_cast<int>(a >> 32)) * 0x1p-31f, &sn, &cs);   // half turns in [-1, 1]
 }
 
 __device__ __forceinline__ float finite_abs(float x) {   // |x|, 0 for infinities and NaN
@@ -113,9 +113,9 @@ __device__ __forceinline__ void kv_insert_piece(const KvInsertArgs& a, const Rop
   float wa[4], wb[4];
   load_bf16x4(a.k_w + ca, wa);
   load_bf16x4(a.k_w + cb, wb);
-  double turns[4];
+  unsigned long long turns[4];
 #pragma unroll
-  for (int u = 0; u < 4; ++u) turns[u] = rot ? tab.turns[ca + u] : 0.0;
+  for (int u = 0; u < 4; ++u) turns[u] = rot ? tab.turns[ca + u] : 0ull;
 
   float ky[KVI_ITERS][8];
   float kmax = 0.f, vmax = 0.f;

@@ -819,11 +819,15 @@ msa_status_t make_code_map(CUtensorMap* m, const void* cache, const msa_config_t
   return make_map(m, cache, 2, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8);
 }
 
-// theta^(-2i/r) / (2 pi) for the rotation pairs
+// theta^(-2i/r) / (2 pi) turns of the rotation pairs, modulo 1, as multiples of 2^-64
 msa::RopeTable rope_table(int rotary_dim, float theta) {
   msa::RopeTable t{};
-  const double l2 = std::log2(static_cast<double>(theta));
-  for (int i = 0; i < rotary_dim / 2; ++i) t.turns[i] = std::exp2(-(2.0 * i / rotary_dim) * l2) * 0.15915494309189533577;
+  long double x = 0.159154943091895335768883763372514362L;
+  const long double step = std::exp2(-2.0L / rotary_dim * std::log2(static_cast<long double>(theta)));
+  for (int i = 0; i < rotary_dim / 2; ++i, x *= step) {
+    const long double f = std::ldexp(x - std::floor(x), 64);
+    t.turns[i] = f < 0x1p64L ? static_cast<unsigned long long>(f) : 0ull;
+  }
   return t;
 }
 
