@@ -1056,6 +1056,7 @@ msa_status_t msa_advance_batch(int32_t num_seqs, int32_t max_blocks_per_seq, int
   CHECK_ARG(delta && ctx_len && page_table && free_ring && pool && ctx_len_out && pool_out && q_start,
             "delta, ctx_len, page_table, free_ring, pool, their outputs and q_start must not be NULL");
   CHECK_ARG(max_rows >= 0 && (slot_map != nullptr || max_rows == 0), "max_rows must be >= 0, and 0 without a slot map");
+  CHECK_SUP(max_rows <= (1 << 30), "max_rows must be <= 2^30");
   CHECK_ARG(aligned4(delta) && aligned4(ctx_len) && aligned4(page_table) && aligned4(free_ring) && aligned4(pool) &&
                 aligned4(ctx_len_out) && aligned4(pool_out) && aligned4(q_start) && aligned4(slot_map),
             "pointers must be 4-byte aligned");
@@ -1074,9 +1075,14 @@ msa_status_t msa_advance_batch(int32_t num_seqs, int32_t max_blocks_per_seq, int
   a.num_pages = num_pages;
   a.max_rows = max_rows;
   const int smem = msa::advance_smem(num_seqs);
-  CUDA_TRY(set_smem(msa::advance_batch_kernel, smem));
+  if (smem > 46 * 1024) CUDA_TRY(set_smem(msa::advance_batch_kernel, smem));   // 48 KiB with the static arrays need no leave
   msa::advance_batch_kernel<<<1, msa::ADV_THREADS, smem, stream>>>(a);
-  return launched();
+  msa_status_t st = launched();
+  if (st != MSA_OK || max_rows <= msa::ADV_ONE) return st;
+  const int per = msa::SLOT_THREADS * msa::SLOT_ROWS;
+  const int grid = std::min((max_rows - 1) / per + 1, 296);
+  CUDA_TRY(launch_overlapped(msa::slot_map_kernel, grid, msa::SLOT_THREADS, static_cast<size_t>(num_seqs + 1) * 4, stream, a));
+  return MSA_OK;
 }
 
 }  // extern "C"

@@ -348,7 +348,8 @@ msa_status_t msa_qknorm_rope_insert_fp8(const msa_config_t* cfg, const msa_batch
  * A length below 0 or above max_blocks_per_seq * 128, a ring state out of range or
  * overfull, or more than max_rows rows end the same way with -1 for the missing
  * pages, and are recorded as MSA_ERR_DEVICE_BOUNDS, as is a page id out of range
- * met on the way (it is written as -1).  num_seqs <= 8192, block_size 128.
+ * met on the way (it is written as -1).  num_seqs <= 8192, block_size 128,
+ * max_rows <= 2^30.
  */
 msa_status_t msa_advance_batch(int32_t num_seqs, int32_t max_blocks_per_seq, int32_t num_pages, int32_t block_size,
                                const int32_t* delta, const int32_t* ctx_len, int32_t* page_table, int32_t* free_ring,

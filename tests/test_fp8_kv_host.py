@@ -101,7 +101,8 @@ def test_advance_refusals(lib):
         return lib.msa_advance_batch(n, width, pages, block, *(ptrs or [P] * 9), rows, None)
     for bad in (dict(n=0), dict(width=0), dict(pages=0), dict(rows=-1)):
         assert call(**bad) == msa.MSA_ERR_INVALID_ARG, bad
-    for bad in (dict(n=8193), dict(width=16385), dict(pages=1 << 24), dict(block=64)):
+    for bad in (dict(n=8193), dict(width=16385), dict(pages=1 << 24), dict(block=64),
+                dict(rows=(1 << 30) + 1)):
         assert call(**bad) == msa.MSA_ERR_UNSUPPORTED, bad
     for i in range(8):
         ptrs = [P] * 9
