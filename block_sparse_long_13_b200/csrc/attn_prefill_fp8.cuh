@@ -479,7 +479,7 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
       for (int k = 0; k < 8; ++k) x[k] = __ldg(p + k * 128);
     };
     // V comes by way of L2: it is wanted soon after K, and from DRAM, beside the partials' stores, a change of bucket
-    // waited up to 12 us for it (2.17 ms a 128K chunk instead of TIMEV).
+    // waited up to 12 us for it.
     auto prefetch_v = [&]() {
       asm volatile("prefetch.global.L2::evict_last [%0];" ::"l"(a.v_cache + (static_cast<long>(row) + ct) * 128));
     };

@@ -787,10 +787,10 @@ msa_status_t check_attn_fp8(const msa_config_t* cfg, const msa_batch_t* batch, c
             "q, caches, out and workspace must be 16-byte aligned");
   CHECK_ARG(aligned4(k_scale) && aligned4(v_scale) && aligned4(block_idx) && aligned4(lse),
             "scales, block_idx and lse must be 4-byte aligned");
-  CHECK_ARG(workspace != nullptr && have >= need, "workspace too small: %zu bytes needed", need);
   CHECK_SUP(static_cast<int64_t>(batch->num_pages) * cfg->num_kv_heads * 128 < (1LL << 31), "the cache has too many rows");
   CHECK_SUP(static_cast<int64_t>(batch->total_q) * cfg->num_kv_heads * cfg->topk < (1LL << 31),
             "too many (row, group, slot) entries");
+  CHECK_ARG(workspace != nullptr && have >= need, "workspace too small: %zu bytes needed", need);
   return MSA_OK;
 }
 
