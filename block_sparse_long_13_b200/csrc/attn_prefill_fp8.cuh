@@ -14,6 +14,7 @@
 #pragma once
 #include "attn_prefill.cuh"
 #include "e4m3.cuh"
+#include "launch_order.cuh"
 
 namespace msa {
 
@@ -100,6 +101,13 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) 
 }
 
 // ------------------------------------------------------------------ schedule
+// An entry is a (row t, group g, slot) with a block; its bucket is (sequence, g, block).  Three kernels turn the
+// entries into tiles of up to 8 of a bucket:
+//   count  every entry's bucket and rank in it (a counter per bucket)
+//   bases  every bucket's run of tiles, ceil(count / 8) of them
+//   place  every entry to tile base + rank / 8, place rank % 8; the first of a tile writes the tile's head
+// The counters' order decides which entries share a tile and where it stands, which no result depends on: an entry's
+// rows of the products are its own.
 struct SchedFp8Args {
   const int32_t* block_idx;   // [total_q][Hkv][topk]
   const int32_t* q_start;
@@ -107,31 +115,33 @@ struct SchedFp8Args {
   const int32_t* page_table;
   const float* k_scale;       // [pages][Hkv]
   const float* v_scale;
-  int* counts;                // [nbuckets], zeroed
-  int* offsets;               // [nbuckets + 1]
-  int* tile_offsets;          // [nbuckets + 1]
-  int* cursor;                // [nbuckets]
-  int* entries;               // [total_q * Hkv * topk]  (t << 6) | slot
-  int* total_tiles;           // [1]
+  int* counts;                // [nbuckets], then the number of tiles; zeroed
+  int* bases;                 // [nbuckets]
+  int2* entries;              // [total_q * Hkv * topk]: bucket (-1: none), rank
   int4* tile_rec;             // [max_tiles][4]: one 64-byte record per tile
   float* part_lse;            // [total_q][Hq][topk]
-  int num_seqs, total_q, Hq, Hkv, topk, max_blocks, nbuckets, num_pages, max_tiles;
+  int num_seqs, total_q, Hq, Hkv, topk, max_blocks, nbuckets, num_pages, max_tiles, cta_rows;
 };
 
-// The count and the scatter of sched_count_scatter_kernel (a CTA's entries are gathered per bucket in a shared hash
-// table first), with what the 8-bit call adds: rows behind the last sequence have no entries, and an entry whose block
-// or page is out of range is recorded and left out (its partial gets lse = -inf in the count).
-__global__ void __launch_bounds__(256) sched_fp8_kernel(const SchedFp8Args a, int pass) {
-  __shared__ int s_key[SCHED_HASH];
-  __shared__ int s_cnt[SCHED_HASH];               // entries per bucket, then (pass 1) the bucket's base
+// Blocks that most rows select (sink-like ones, each row's own block) would take thousands of atomics on one address, so
+// a CTA first gathers its rows' entries per bucket in a shared-memory hash table and adds once per bucket.  Rows behind
+// the last sequence have no entries; an entry whose block or page is out of range is recorded and left out (its partial
+// gets lse = -inf).
+constexpr int SCH8_HASH = 4096;                  // table slots: >= 2 x a CTA's entries when it is used
+constexpr int SCH8_EPT = SCH8_HASH / 2 / 256;    // entries per thread (256 threads)
+
+__global__ void __launch_bounds__(256) sched_fp8_count_kernel(const SchedFp8Args a) {
+  __shared__ int s_key[SCH8_HASH];
+  __shared__ int s_cnt[SCH8_HASH];               // entries per bucket, then the bucket's base
+  pdl_launch_dependents();
   const int rows = min(a.total_q, __ldg(a.q_start + a.num_seqs));
-  const int t0 = blockIdx.x * SCHED_ROWS;
-  const int t1 = min(rows, t0 + SCHED_ROWS);
+  const int t0 = blockIdx.x * a.cta_rows;
+  const int t1 = min(rows, t0 + a.cta_rows);
   if (t0 >= t1) return;
   const int per_row = a.Hkv * a.topk;
   const int nent = (t1 - t0) * per_row;
   const long e0 = static_cast<long>(t0) * per_row;
-  auto bucket_of = [&](int el, int& ent) -> int {
+  auto bucket_of = [&](int el) -> int {
     const int b = __ldg(a.block_idx + e0 + el);
     if (b < 0) return -1;
     const int t = t0 + el / per_row, rem = el % per_row, g = rem / a.topk, slot = rem % a.topk;
@@ -140,91 +150,118 @@ __global__ void __launch_bounds__(256) sched_fp8_kernel(const SchedFp8Args a, in
     int page = -1;
     if (b < a.max_blocks && b * 128 <= p) page = __ldg(a.page_table + static_cast<long>(s) * a.max_blocks + b);
     if (page < 0 || page >= a.num_pages) {
-      if (pass == 0) {
-        flag_error(MSA_DEV_BOUNDS);
-        for (int h = 0; h < ATTP_G; ++h) a.part_lse[(static_cast<long>(t) * a.Hq + g * ATTP_G + h) * a.topk + slot] = -INFINITY;
-      }
+      flag_error(MSA_DEV_BOUNDS);
+      for (int h = 0; h < ATTP_G; ++h) a.part_lse[(static_cast<long>(t) * a.Hq + g * ATTP_G + h) * a.topk + slot] = -INFINITY;
       return -1;
     }
-    ent = (t << 6) | slot;
     return (s * a.Hkv + g) * a.max_blocks + b;
   };
-  if (2 * SCHED_ROWS * per_row > SCHED_HASH) {    // rows too wide for the table: one atomic per entry
+  if (nent > SCH8_HASH / 2) {                     // rows too wide for the table: one atomic per entry
     for (int el = threadIdx.x; el < nent; el += blockDim.x) {
-      int ent = 0;
-      const int bk = bucket_of(el, ent);
-      if (bk < 0) continue;
-      if (pass == 0) atomicAdd(&a.counts[bk], 1);
-      else a.entries[atomicAdd(&a.cursor[bk], 1)] = ent;
+      const int bk = bucket_of(el);
+      a.entries[e0 + el] = make_int2(bk, bk < 0 ? 0 : atomicAdd(&a.counts[bk], 1));
     }
     return;
   }
-  for (int i = threadIdx.x; i < SCHED_HASH; i += blockDim.x) { s_key[i] = -1; s_cnt[i] = 0; }
+  for (int i = threadIdx.x; i < SCH8_HASH; i += blockDim.x) { s_key[i] = -1; s_cnt[i] = 0; }
   __syncthreads();
-  int hs[SCHED_EPT], li[SCHED_EPT], ents[SCHED_EPT];
+  int bks[SCH8_EPT], hs[SCH8_EPT], li[SCH8_EPT];
 #pragma unroll
-  for (int k = 0; k < SCHED_EPT; ++k) {
+  for (int k = 0; k < SCH8_EPT; ++k) {
+    const int el = threadIdx.x + k * 256;
+    bks[k] = el < nent ? bucket_of(el) : -1;
+  }
+#pragma unroll
+  for (int k = 0; k < SCH8_EPT; ++k) {
     hs[k] = -1;
     li[k] = 0;
-    ents[k] = 0;
-    const int el = threadIdx.x + k * 256;
-    if (el >= nent) continue;
-    const int bk = bucket_of(el, ents[k]);
-    if (bk < 0) continue;
-    uint32_t h = (static_cast<uint32_t>(bk) * 2654435761u) >> 20;   // 12 bits
-    for (int probe = 0; probe < SCHED_HASH; ++probe) {               // the table is at most half full
-      const int prev = atomicCAS(&s_key[h], -1, bk);
-      if (prev == -1 || prev == bk) { hs[k] = static_cast<int>(h); break; }
-      h = (h + 1) & (SCHED_HASH - 1);
+    if (bks[k] < 0) continue;
+    uint32_t h = (static_cast<uint32_t>(bks[k]) * 2654435761u) >> 20;   // 12 bits
+    for (int probe = 0; probe < SCH8_HASH; ++probe) {                    // the table is at most half full
+      const int prev = atomicCAS(&s_key[h], -1, bks[k]);
+      if (prev == -1 || prev == bks[k]) { hs[k] = static_cast<int>(h); break; }
+      h = (h + 1) & (SCH8_HASH - 1);
     }
     if (hs[k] >= 0) li[k] = atomicAdd(&s_cnt[hs[k]], 1);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < SCHED_HASH; i += blockDim.x) {
+  for (int i = threadIdx.x; i < SCH8_HASH; i += blockDim.x) {
     const int bk = s_key[i];
-    if (bk < 0) continue;
-    if (pass == 0) atomicAdd(&a.counts[bk], s_cnt[i]);
-    else s_cnt[i] = atomicAdd(&a.cursor[bk], s_cnt[i]);
+    if (bk >= 0) s_cnt[i] = atomicAdd(&a.counts[bk], s_cnt[i]);
   }
-  if (pass == 0) return;
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < SCHED_EPT; ++k)
-    if (hs[k] >= 0) a.entries[s_cnt[hs[k]] + li[k]] = ents[k];
+  for (int k = 0; k < SCH8_EPT; ++k) {
+    const int el = threadIdx.x + k * 256;
+    if (el < nent) a.entries[e0 + el] = make_int2(bks[k], hs[k] >= 0 ? s_cnt[hs[k]] + li[k] : 0);
+  }
 }
 
-// One 64-byte record per tile:
+// CTA = 1024 buckets, thread = 4: their tiles' exclusive sums over the CTA, whose run begins where the number of tiles
+// stood.
+__global__ void __launch_bounds__(256) sched_fp8_bases_kernel(const SchedFp8Args a) {
+  __shared__ int s_w[8], s_base;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int i0 = (blockIdx.x * 256 + tid) * 4;
+  int tl[4], sum = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    tl[k] = i0 + k < a.nbuckets ? (a.counts[i0 + k] + ATTP_TOK - 1) / ATTP_TOK : 0;
+    sum += tl[k];
+  }
+  int v = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int n = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    if (lane >= o) v += n;
+  }
+  if (lane == 31) s_w[warp] = v;
+  __syncthreads();
+  if (tid == 0) {
+    int total = 0;
+    for (int w = 0; w < 8; ++w) { const int n = s_w[w]; s_w[w] = total; total += n; }
+    s_base = total ? atomicAdd(a.counts + a.nbuckets, total) : 0;
+  }
+  __syncthreads();
+  int at = s_base + s_w[warp] + v - sum;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (i0 + k < a.nbuckets) a.bases[i0 + k] = at;
+    at += tl[k];
+  }
+}
+
+// A tile's 64-byte record:
 //   int[0] bucket, [1] first row of the block in the cache = (page * Hkv + g) * 128, [2] g, [3] b, [4] position offset of
 //   the sequence (p = t + off), [5] entries n | tokens of the block that the sequence holds << 8, [6], [7] the block's K
-//   and V scale, [8 .. 8+n) entries (t << 6 | slot).
-__global__ void __launch_bounds__(256) sched_fp8_tiles_kernel(const SchedFp8Args a) {
-  const int T = min(a.total_tiles[0], a.max_tiles);
-  for (int tile = blockIdx.x * blockDim.x + threadIdx.x; tile < T; tile += gridDim.x * blockDim.x) {
-    int lo = 0, hi = a.nbuckets - 1;  // largest bucket with tile_offsets[bucket] <= tile
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (__ldg(a.tile_offsets + mid) <= tile) lo = mid; else hi = mid - 1;
-    }
-    const int b = lo % a.max_blocks, g = (lo / a.max_blocks) % a.Hkv, seq = lo / (a.max_blocks * a.Hkv);
-    const int e0 = __ldg(a.offsets + lo) + (tile - __ldg(a.tile_offsets + lo)) * ATTP_TOK;
-    const int n = min(ATTP_TOK, __ldg(a.offsets + lo + 1) - e0);
-    const int page = __ldg(a.page_table + static_cast<long>(seq) * a.max_blocks + b);   // checked by the count
-    const int row = page * a.Hkv + g, ctx = __ldg(a.ctx_len + seq);
-    int ent[ATTP_TOK];
-#pragma unroll
-    for (int e = 0; e < ATTP_TOK; ++e) ent[e] = e < n ? a.entries[e0 + e] : 0;
-    int4* r = a.tile_rec + static_cast<long>(tile) * 4;
-    r[0] = make_int4(lo, row * 128, g, b);
-    r[1] = make_int4(ctx - __ldg(a.q_start + seq + 1), n | (min(128, ctx - b * 128) << 8),
-                     __float_as_int(__ldg(a.k_scale + row)), __float_as_int(__ldg(a.v_scale + row)));
-    r[2] = make_int4(ent[0], ent[1], ent[2], ent[3]);
-    r[3] = make_int4(ent[4], ent[5], ent[6], ent[7]);
-  }
+//   and V scale, [8 .. 8+n) entries (t << 6 | slot), the rest of them whatever it was.
+__global__ void __launch_bounds__(256) sched_fp8_place_kernel(const SchedFp8Args a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int per_row = a.Hkv * a.topk;
+  const long e = static_cast<long>(blockIdx.x) * 256 + threadIdx.x;
+  if (e >= static_cast<long>(min(a.total_q, __ldg(a.q_start + a.num_seqs))) * per_row) return;
+  const int2 x = a.entries[e];
+  if (x.x < 0) return;
+  const int t = static_cast<int>(e / per_row), slot = static_cast<int>(e % a.topk);
+  int4* r = a.tile_rec + static_cast<long>(a.bases[x.x] + x.y / ATTP_TOK) * 4;
+  const int place = x.y % ATTP_TOK;
+  reinterpret_cast<int*>(r + 2)[place] = (t << 6) | slot;
+  if (place != 0) return;
+  const int n = min(ATTP_TOK, a.counts[x.x] - x.y);
+  const int b = x.x % a.max_blocks, g = (x.x / a.max_blocks) % a.Hkv, seq = x.x / (a.max_blocks * a.Hkv);
+  const int page = __ldg(a.page_table + static_cast<long>(seq) * a.max_blocks + b);   // checked by the count
+  const int row = page * a.Hkv + g, ctx = __ldg(a.ctx_len + seq);
+  r[0] = make_int4(x.x, row * 128, g, b);
+  r[1] = make_int4(ctx - __ldg(a.q_start + seq + 1), n | (min(128, ctx - b * 128) << 8),
+                   __float_as_int(__ldg(a.k_scale + row)), __float_as_int(__ldg(a.v_scale + row)));
 }
 
 // ------------------------------------------------------------------ tiles
 struct AttnPrefillFp8Args {
-  const int4* tile_rec;      // [tiles][4] records written by sched_fp8_tiles_kernel
+  const int4* tile_rec;      // [tiles][4] records written by sched_fp8_place_kernel
   const int* total_tiles;
   const uint8_t* k_cache;    // [pages][Hkv][128][128] codes
   const uint8_t* v_cache;
@@ -283,10 +320,12 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
   tc_fence_after();
   const uint32_t tmem = s_tmem;
 
+  pdl_launch_dependents();
+  pdl_wait();                                            // the records
   // The tile list is cut into ATTP_PHASES equal phases (about one KV group each for a
   // single-sequence prefill); every CTA takes a contiguous share of each phase in turn,
   // so at any time all CTAs gather query rows of the same phase and those rows stay in L2.
-  const int T = min(__ldg(a.total_tiles), a.max_tiles);
+  const int T = min(*a.total_tiles, a.max_tiles);
   static_assert(ATTP_PHASES == 4, "the phase map below is written out for 4 phases");
   auto share = [&](int q, int& start, int& cnt) {
     const long p0 = static_cast<long>(T) * q / ATTP_PHASES, p1 = static_cast<long>(T) * (q + 1) / ATTP_PHASES;
@@ -412,7 +451,10 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
       if (i + 1 < ntile) nbucket = __ldg(&a.tile_rec[static_cast<long>(tile_of(i + 1)) * 4].x);
       const bool change = bucket != cur_bucket;
       if (change) {
-        if (cur_bucket >= 0) umma_commit(&k_empty);       // the previous bucket's last S is issued, its last P V not yet
+        // the previous bucket's last S is issued: K may be replaced, and its last P V does not wait for that
+        if (cur_bucket >= 0) umma_commit(&k_empty);
+        if (pv_pending && !issue_pv(i - 1, true)) break;
+        pv_pending = false;
         if (!mbar_wait(&k_full, kvit & 1, &s_abort)) break;
         ++kvit;
         cur_bucket = bucket;
@@ -430,7 +472,7 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
       umma_commit(&s_full[sb]);
       umma_commit(&q_empty[qb]);
       if (++qb == ATTP_QBUF) { qb = 0; qph ^= 1u; }
-      if (pv_pending) ok = issue_pv(i - 1, change);
+      if (pv_pending) ok = issue_pv(i - 1, false);
       pv_pending = true;
     }
     if (ok && !s_abort && pv_pending) issue_pv(ntile - 1, true);
@@ -489,9 +531,10 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
       prefetch_v();
     }
     for (uint32_t it = 0; have && ok; ++it) {
+      const bool nans = warp_has_nan(x);
       ok = mbar_wait_warp(&k_empty, (it & 1) ^ 1, &s_abort);
       if (!ok) break;
-      if (warp_has_nan(x)) {                     // rare: piece by piece, out of L2 again
+      if (nans) {                     // rare: piece by piece, out of L2 again
 #pragma unroll 1
         for (int k = 0; k < 8; ++k) widen16_bf16<true>(k_s, k * 128 + ct, __ldg(codes(a.k_cache) + k * 128));
       } else {
@@ -707,6 +750,7 @@ struct MergeFp8Args {
 __global__ void __launch_bounds__(256) attn_merge_fp8_kernel(const MergeFp8Args a) {
   __shared__ float s_w[ATTP_G][MRG_MAXK];   // per head and slot: exp(lse - max), or -1 (no partial)
   const int t = blockIdx.x / a.Hkv, g = blockIdx.x % a.Hkv;
+  pdl_wait();                               // the partials
   if (t >= __ldg(a.q_start + a.num_seqs)) return;
   const int h = threadIdx.x >> 4, d8 = threadIdx.x & 15;
   const int head = g * ATTP_G + h;

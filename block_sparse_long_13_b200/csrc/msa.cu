@@ -819,6 +819,28 @@ msa_status_t make_code_map(CUtensorMap* m, const void* cache, const msa_config_t
   return make_map(m, cache, 2, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8);
 }
 
+struct PrefillFp8Ws {
+  size_t counts, bases, tile_rec, part_lse, part_o, bytes;
+  int64_t entries, nbuckets, max_tiles;
+};
+
+// The entries' buckets and ranks lie where the partials come later (256 x 16 bytes an entry).
+PrefillFp8Ws prefill_fp8_plan(const msa_config_t* c, const msa_batch_t* b) {
+  PrefillFp8Ws w{};
+  w.nbuckets = static_cast<int64_t>(b->num_seqs) * c->num_kv_heads * b->max_blocks_per_seq;
+  w.entries = static_cast<int64_t>(b->total_q) * c->num_kv_heads * c->topk;
+  w.max_tiles = (w.entries + msa::ATTP_TOK - 1) / msa::ATTP_TOK + std::min(w.nbuckets, w.entries);
+  size_t o = 0;
+  auto take = [&](size_t n) { size_t at = o; o = align_up(o + n, 256); return at; };
+  w.counts = take((w.nbuckets + 1) * 4);
+  w.bases = take(w.nbuckets * 4);
+  w.tile_rec = take(static_cast<size_t>(w.max_tiles) * 64);
+  w.part_lse = take(static_cast<size_t>(b->total_q) * c->num_q_heads * c->topk * 4);
+  w.part_o = take(static_cast<size_t>(b->total_q) * c->topk * c->num_q_heads * c->head_dim * 2);
+  w.bytes = o;
+  return w;
+}
+
 // theta^(-2i/r) / (2 pi) turns of the rotation pairs, modulo 1, as multiples of 2^-64
 msa::RopeTable rope_table(int rotary_dim, float theta) {
   msa::RopeTable t{};
@@ -841,7 +863,8 @@ size_t msa_decode_fp8_workspace_bytes(const msa_config_t* cfg, const msa_batch_t
 }
 
 size_t msa_prefill_fp8_workspace_bytes(const msa_config_t* cfg, const msa_batch_t* batch) {
-  return msa_prefill_workspace_bytes(cfg, batch);   // the same schedule and partials
+  if (check_config(cfg) != MSA_OK || check_batch(batch) != MSA_OK) return 0;
+  return prefill_fp8_plan(cfg, batch).bytes;
 }
 
 msa_status_t msa_attn_decode_fp8(const msa_config_t* cfg, const msa_batch_t* batch, const void* q,
@@ -892,8 +915,8 @@ msa_status_t msa_attn_prefill_fp8(const msa_config_t* cfg, const msa_batch_t* ba
   msa_status_t st = check_attn_fp8(cfg, batch, q, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale, block_idx, out, lse,
                                    workspace, workspace_bytes, msa_prefill_fp8_workspace_bytes(cfg, batch));
   if (st != MSA_OK) return st;
-  const PrefillWs w = prefill_plan(cfg, batch);
-  CHECK_SUP(w.nbuckets < (1L << 31) && w.max_tiles < (1L << 31), "too many (sequence, group, block) buckets");
+  const PrefillFp8Ws w = prefill_fp8_plan(cfg, batch);
+  CHECK_SUP(w.nbuckets < (1L << 31) - 1024 && w.max_tiles < (1L << 31), "too many (sequence, group, block) buckets");
   if (batch->total_q == 0) return MSA_OK;
   char* ws = static_cast<char*>(workspace);
   const int Hq = cfg->num_q_heads, Hkv = cfg->num_kv_heads, k = cfg->topk;
@@ -905,11 +928,8 @@ msa_status_t msa_attn_prefill_fp8(const msa_config_t* cfg, const msa_batch_t* ba
   s.k_scale = k_scale;
   s.v_scale = v_scale;
   s.counts = reinterpret_cast<int*>(ws + w.counts);
-  s.offsets = reinterpret_cast<int*>(ws + w.offsets);
-  s.tile_offsets = reinterpret_cast<int*>(ws + w.tile_offsets);
-  s.cursor = reinterpret_cast<int*>(ws + w.cursor);
-  s.entries = reinterpret_cast<int*>(ws + w.entries);
-  s.total_tiles = reinterpret_cast<int*>(ws + w.total_tiles);
+  s.bases = reinterpret_cast<int*>(ws + w.bases);
+  s.entries = reinterpret_cast<int2*>(ws + w.part_o);
   s.tile_rec = reinterpret_cast<int4*>(ws + w.tile_rec);
   s.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
   s.num_seqs = batch->num_seqs;
@@ -921,26 +941,14 @@ msa_status_t msa_attn_prefill_fp8(const msa_config_t* cfg, const msa_batch_t* ba
   s.nbuckets = static_cast<int>(w.nbuckets);
   s.num_pages = batch->num_pages;
   s.max_tiles = static_cast<int>(w.max_tiles);
-  msa::SchedArgs scan{};
-  scan.counts = s.counts;
-  scan.offsets = s.offsets;
-  scan.tile_offsets = s.tile_offsets;
-  scan.cursor = s.cursor;
-  scan.total_tiles = s.total_tiles;
-  scan.nbuckets = s.nbuckets;
-  CUDA_TRY(cudaMemsetAsync(s.counts, 0, w.nbuckets * 4, stream));
-  const unsigned sgrid = static_cast<unsigned>((batch->total_q + msa::SCHED_ROWS - 1) / msa::SCHED_ROWS);
-  msa::sched_fp8_kernel<<<sgrid, 256, 0, stream>>>(s, 0);
+  // few rows: eight to a CTA, so that its chain of look-ups is short; many: 32, so that hot blocks take fewer atomics
+  s.cta_rows = batch->total_q <= 32 * msa::ATD8_GRID ? 8 : 32;
+  CUDA_TRY(cudaMemsetAsync(s.counts, 0, (w.nbuckets + 1) * 4, stream));
+  msa::sched_fp8_count_kernel<<<static_cast<unsigned>((batch->total_q + s.cta_rows - 1) / s.cta_rows), 256, 0, stream>>>(s);
   if ((st = launched()) != MSA_OK) return st;
-  msa::sched_scan_kernel<<<1, 1024, 0, stream>>>(scan);
-  if ((st = launched()) != MSA_OK) return st;
-  msa::sched_fp8_kernel<<<sgrid, 256, 0, stream>>>(s, 1);
-  if ((st = launched()) != MSA_OK) return st;
+  CUDA_TRY(launch_overlapped(msa::sched_fp8_bases_kernel, static_cast<unsigned>((w.nbuckets + 1023) / 1024), 256, 0, stream, s));
+  CUDA_TRY(launch_overlapped(msa::sched_fp8_place_kernel, static_cast<unsigned>((w.entries + 255) / 256), 256, 0, stream, s));
   const int sms = num_sms();
-  const long tgrid = std::min<long>((w.max_tiles + 255) / 256, 8L * sms);
-  msa::sched_fp8_tiles_kernel<<<static_cast<unsigned>(std::max<long>(1, tgrid)), 256, 0, stream>>>(s);
-  if ((st = launched()) != MSA_OK) return st;
-
   CUtensorMap tq, tpo;
   {
     const uint64_t dims[2] = {128, static_cast<uint64_t>(batch->total_q) * Hq};
@@ -952,7 +960,7 @@ msa_status_t msa_attn_prefill_fp8(const msa_config_t* cfg, const msa_batch_t* ba
   }
   msa::AttnPrefillFp8Args a{};
   a.tile_rec = s.tile_rec;
-  a.total_tiles = s.total_tiles;
+  a.total_tiles = s.counts + w.nbuckets;
   a.k_cache = static_cast<const uint8_t*>(k_cache_e4m3);
   a.v_cache = static_cast<const uint8_t*>(v_cache_e4m3);
   a.part_lse = s.part_lse;
@@ -961,8 +969,7 @@ msa_status_t msa_attn_prefill_fp8(const msa_config_t* cfg, const msa_batch_t* ba
   a.max_tiles = s.max_tiles;
   a.scale_log2 = softmax_scale(cfg) * 1.4426950408889634f;
   CUDA_TRY(set_smem(msa::attn_prefill_fp8_kernel, msa::ATTP_SMEM));
-  msa::attn_prefill_fp8_kernel<<<sms, msa::ATP8_THREADS, msa::ATTP_SMEM, stream>>>(tq, tpo, a);
-  if ((st = launched()) != MSA_OK) return st;
+  CUDA_TRY(launch_overlapped(msa::attn_prefill_fp8_kernel, sms, msa::ATP8_THREADS, msa::ATTP_SMEM, stream, tq, tpo, a));
   msa::MergeFp8Args m{};
   m.part_o = reinterpret_cast<const __nv_bfloat16*>(ws + w.part_o);
   m.part_lse = s.part_lse;
@@ -974,8 +981,8 @@ msa_status_t msa_attn_prefill_fp8(const msa_config_t* cfg, const msa_batch_t* ba
   m.Hq = Hq;
   m.Hkv = Hkv;
   m.topk = k;
-  msa::attn_merge_fp8_kernel<<<static_cast<unsigned>(batch->total_q) * Hkv, 256, 0, stream>>>(m);
-  return launched();
+  CUDA_TRY(launch_overlapped(msa::attn_merge_fp8_kernel, static_cast<unsigned>(batch->total_q) * Hkv, 256, 0, stream, m));
+  return MSA_OK;
 }
 
 msa_status_t msa_qknorm_rope_insert_fp8(const msa_config_t* cfg, const msa_batch_t* batch, const void* q,
