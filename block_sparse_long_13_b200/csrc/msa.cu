@@ -841,39 +841,11 @@ PrefillFp8Ws prefill_fp8_plan(const msa_config_t* c, const msa_batch_t* b) {
   return w;
 }
 
-// theta^(-2i/r) / (2 pi) turns of the rotation pairs, modulo 1, as multiples of 2^-64
-msa::RopeTable rope_table(int rotary_dim, float theta) {
-  msa::RopeTable t{};
-  long double x = 0.159154943091895335768883763372514362L;
-  const long double step = std::exp2(-2.0L / rotary_dim * std::log2(static_cast<long double>(theta)));
-  for (int i = 0; i < rotary_dim / 2; ++i, x *= step) {
-    const long double f = std::ldexp(x - std::floor(x), 64);
-    t.turns[i] = f < 0x1p64L ? static_cast<unsigned long long>(f) : 0ull;
-  }
-  return t;
-}
-
-}  // namespace
-
-extern "C" {
-
-size_t msa_decode_fp8_workspace_bytes(const msa_config_t* cfg, const msa_batch_t* batch) {
-  if (check_config(cfg) != MSA_OK || check_batch(batch) != MSA_OK) return 0;
-  return static_cast<size_t>(msa::ATD8_GRID) * 2 * msa::ATD8_PART * 4;
-}
-
-size_t msa_prefill_fp8_workspace_bytes(const msa_config_t* cfg, const msa_batch_t* batch) {
-  if (check_config(cfg) != MSA_OK || check_batch(batch) != MSA_OK) return 0;
-  return prefill_fp8_plan(cfg, batch).bytes;
-}
-
-msa_status_t msa_attn_decode_fp8(const msa_config_t* cfg, const msa_batch_t* batch, const void* q,
-                                 const void* k_cache_e4m3, const void* v_cache_e4m3, const float* k_scale,
-                                 const float* v_scale, const int32_t* block_idx, void* out, float* lse, void* workspace,
-                                 size_t workspace_bytes, cudaStream_t stream) {
-  msa_status_t st = check_attn_fp8(cfg, batch, q, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale, block_idx, out, lse,
-                                   workspace, workspace_bytes, msa_decode_fp8_workspace_bytes(cfg, batch));
-  if (st != MSA_OK || batch->total_q == 0) return st;
+// The row-major form, a stream of (row, group, block) slots.
+msa_status_t run_decode_fp8(const msa_config_t* cfg, const msa_batch_t* batch, const void* q, const void* k_cache_e4m3,
+                            const void* v_cache_e4m3, const float* k_scale, const float* v_scale,
+                            const int32_t* block_idx, void* out, float* lse, void* workspace, cudaStream_t stream) {
+  msa_status_t st;
   msa::AttnDecodeFp8Args a{};
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.k_scale = k_scale;
@@ -908,6 +880,52 @@ msa_status_t msa_attn_decode_fp8(const msa_config_t* cfg, const msa_batch_t* bat
   return MSA_OK;
 }
 
+// Which form a prefill call takes.  The tiles' schedule, launches and merge cost about 40 us before the first tile;
+// the slots cost 0.65 us a block and CTA, and about six blocks' time more a (row, group).  Measured, us, slots / tiles:
+// 16 blocks a row, 4 groups: 128 rows 46 / 70 and 45 / 62 (32K and 4K contexts), 256 rows 81 / 94 and 81 / 89, 512 rows
+// 151 / 146 and 151 / 119; 4 blocks a row, one group: 1024 rows 34 / 42, 2048 rows 63 / 57; one block a row, 4 groups:
+// 1024 rows 64 / 54.
+bool few_slots(const msa_config_t* c, const msa_batch_t* b) {
+  const int64_t units = static_cast<int64_t>(b->total_q) * c->num_kv_heads;
+  return units * (c->topk + 10) <= 27000;
+}
+
+// theta^(-2i/r) / (2 pi) turns of the rotation pairs, modulo 1, as multiples of 2^-64
+msa::RopeTable rope_table(int rotary_dim, float theta) {
+  msa::RopeTable t{};
+  long double x = 0.159154943091895335768883763372514362L;
+  const long double step = std::exp2(-2.0L / rotary_dim * std::log2(static_cast<long double>(theta)));
+  for (int i = 0; i < rotary_dim / 2; ++i, x *= step) {
+    const long double f = std::ldexp(x - std::floor(x), 64);
+    t.turns[i] = f < 0x1p64L ? static_cast<unsigned long long>(f) : 0ull;
+  }
+  return t;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t msa_decode_fp8_workspace_bytes(const msa_config_t* cfg, const msa_batch_t* batch) {
+  if (check_config(cfg) != MSA_OK || check_batch(batch) != MSA_OK) return 0;
+  return static_cast<size_t>(msa::ATD8_GRID) * 2 * msa::ATD8_PART * 4;
+}
+
+size_t msa_prefill_fp8_workspace_bytes(const msa_config_t* cfg, const msa_batch_t* batch) {
+  if (check_config(cfg) != MSA_OK || check_batch(batch) != MSA_OK) return 0;
+  return few_slots(cfg, batch) ? msa_decode_fp8_workspace_bytes(cfg, batch) : prefill_fp8_plan(cfg, batch).bytes;
+}
+
+msa_status_t msa_attn_decode_fp8(const msa_config_t* cfg, const msa_batch_t* batch, const void* q,
+                                 const void* k_cache_e4m3, const void* v_cache_e4m3, const float* k_scale,
+                                 const float* v_scale, const int32_t* block_idx, void* out, float* lse, void* workspace,
+                                 size_t workspace_bytes, cudaStream_t stream) {
+  msa_status_t st = check_attn_fp8(cfg, batch, q, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale, block_idx, out, lse,
+                                   workspace, workspace_bytes, msa_decode_fp8_workspace_bytes(cfg, batch));
+  if (st != MSA_OK || batch->total_q == 0) return st;
+  return run_decode_fp8(cfg, batch, q, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale, block_idx, out, lse, workspace, stream);
+}
+
 msa_status_t msa_attn_prefill_fp8(const msa_config_t* cfg, const msa_batch_t* batch, const void* q,
                                   const void* k_cache_e4m3, const void* v_cache_e4m3, const float* k_scale,
                                   const float* v_scale, const int32_t* block_idx, void* out, float* lse, void* workspace,
@@ -918,6 +936,8 @@ msa_status_t msa_attn_prefill_fp8(const msa_config_t* cfg, const msa_batch_t* ba
   const PrefillFp8Ws w = prefill_fp8_plan(cfg, batch);
   CHECK_SUP(w.nbuckets < (1L << 31) - 1024 && w.max_tiles < (1L << 31), "too many (sequence, group, block) buckets");
   if (batch->total_q == 0) return MSA_OK;
+  if (few_slots(cfg, batch))
+    return run_decode_fp8(cfg, batch, q, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale, block_idx, out, lse, workspace, stream);
   char* ws = static_cast<char*>(workspace);
   const int Hq = cfg->num_q_heads, Hkv = cfg->num_kv_heads, k = cfg->topk;
   msa::SchedFp8Args s{};

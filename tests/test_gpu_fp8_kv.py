@@ -28,15 +28,22 @@ pytestmark = pytest.mark.gpu
 LSE_ABS = 2.5e-4
 ATTN = {"decode": msa.attn_decode_fp8, "prefill": msa.attn_prefill_fp8}
 WORKSPACE = {"decode": msa.decode_fp8_workspace_bytes, "prefill": msa.prefill_fp8_workspace_bytes}
+# a prefill call of few rows takes the decode form: "tiles" are prefill calls with a long sequence more
+FORMS = ["decode", "prefill", "tiles"]
+BALLAST = 2600
 
 
 # ----------------------------------------------------------------- attention
 class Case:
-    def __init__(self, seed, ctx, nq, kv=4, topk=16, pad=0, extra_width=0, empty=(), q_size=1.0):
+    def __init__(self, seed, ctx, nq, which="decode", kv=4, topk=16, pad=0, extra_width=0, empty=(), q_size=1.0):
         rng = np.random.default_rng(seed)
+        self.fn, self.size = ATTN.get(which, msa.attn_prefill_fp8), WORKSPACE.get(which, msa.prefill_fp8_workspace_bytes)
+        self.main = sum(nq)                        # rows of the sequences that the test is about
+        if which == "tiles":
+            ctx, nq = list(ctx) + [BALLAST], list(nq) + [BALLAST]
         self.kv, self.topk, self.ctx, self.nq = kv, topk, ctx, nq
         starts = np.concatenate([[0], np.cumsum(nq)])
-        self.rows = int(starts[-1])
+        self.rows, self.starts = int(starts[-1]), starts
         width = max(-(-c // 128) for c in ctx) + extra_width
         need = sum(-(-c // 128) for c in ctx)
         self.pages = need + 2
@@ -81,16 +88,17 @@ class Case:
                        grow(torch.from_numpy(self.sel)).contiguous().cuda()]
         return self._d
 
-    def run(self, which, lse=True, stream=None):
+    def run(self, lse=True, stream=None):
         d = self.device()
         out = torch.full_like(d[0], 7.0)
         l = torch.full(d[0].shape[:2], 7.0, device="cuda") if lse else None
-        ws = torch.full((WORKSPACE[which](self.cfg, self.batch),), 0xFF, dtype=torch.uint8, device="cuda")
-        ATTN[which](self.cfg, self.batch, *d, out, l, ws, stream=stream)
+        ws = torch.full((self.size(self.cfg, self.batch),), 0xFF, dtype=torch.uint8, device="cuda")
+        self.fn(self.cfg, self.batch, *d, out, l, ws, stream=stream)
         return out, l
 
     def check(self, out, lse, rows=None):
-        rows = range(self.rows) if rows is None else rows
+        if rows is None:
+            rows = [*range(0, self.main, max(1, self.main // 200)), *range(self.main, self.rows, 97)]
         rows = np.asarray(list(rows))
         ref, ref_lse, mag = K.attention(self.q[rows].double().numpy(), K.values(self.k, self.ks), K.values(self.v, self.vs),
                                         self.seq[rows], self.pos[rows], self.sel[rows], self.table)
@@ -121,85 +129,119 @@ SHAPES = {
 }
 
 
-@pytest.mark.parametrize("which", ["decode", "prefill"])
+@pytest.mark.parametrize("which", FORMS)
 @pytest.mark.parametrize("shape", SHAPES)
 def test_attention_matches_oracle(cuda_ok, shape, which):
-    c = Case(3, **SHAPES[shape])
-    out, lse = c.run(which)
+    c = Case(3, which=which, **SHAPES[shape])
+    out, lse = c.run()
     assert msa.device_status() == msa.MSA_OK
-    c.check(out, lse, range(0, c.rows, max(1, c.rows // 200)))
+    c.check(out, lse)
 
 
-@pytest.mark.parametrize("which", ["decode", "prefill"])
+@pytest.mark.parametrize("which", FORMS)
 def test_rows_without_keys_and_padded_rows(cuda_ok, which):
     """A selection of -1 only gives out 0 and lse -inf; rows behind the last sequence stay as they were."""
-    c = Case(4, ctx=[1000, 40, 2000], nq=[4, 2, 3], pad=5, empty=[(0, 0), (0, 1), (0, 2), (0, 3), (4, 2), (8, 3), (5, 0)])
-    out, lse = c.run(which)
+    c = Case(4, ctx=[1000, 40, 2000], nq=[4, 2, 3], which=which, pad=5, empty=[(0, 0), (0, 1), (0, 2), (0, 3), (4, 2), (8, 3), (5, 0)])
+    out, lse = c.run()
     assert msa.device_status() == msa.MSA_OK
     c.check(out[:c.rows], lse[:c.rows])
     assert (out[c.rows:] == 7.0).all() and (lse[c.rows:] == 7.0).all()
 
 
-@pytest.mark.parametrize("which", ["decode", "prefill"])
+@pytest.mark.parametrize("which", FORMS)
 def test_holes_and_order_of_the_selection_do_not_matter(cuda_ok, which):
     """-1 anywhere in a row and ids in any order; without lse."""
-    c = Case(5, ctx=[3000, 700], nq=[3, 2], topk=16)
+    c = Case(5, ctx=[3000, 700], nq=[3, 2], which=which, topk=16)
     rng = np.random.default_rng(0)
     for t in range(c.rows):
         for g in range(c.kv):
             c.sel[t, g] = rng.permutation(c.sel[t, g])
             c.sel[t, g, rng.integers(0, 16, size=3)] = -1
-    out, _ = c.run(which, lse=False)
+    out, _ = c.run(lse=False)
     assert msa.device_status() == msa.MSA_OK
     c.check(out, None)
 
 
-@pytest.mark.parametrize("which", ["decode", "prefill"])
+@pytest.mark.parametrize("which", FORMS)
 @pytest.mark.parametrize("q_size", [1e-30, 1e-3, 4.0])
 def test_query_sizes(cuda_ok, which, q_size):
     """Queries from tiny to large, a head of zeros, elements 2^-12 below their head's largest."""
-    c = Case(6, ctx=[900, 130], nq=[2, 2], kv=2, topk=4, q_size=q_size)
+    c = Case(6, ctx=[900, 130], nq=[2, 2], which=which, kv=2, topk=4, q_size=q_size)
     c.q[0, 3] = 0
     c.q[1, 5, ::2] *= 2.0 ** -12
     if q_size > 1:                      # logits in the hundreds: an fp32 sum's bound grows with them
         c.ks *= 0.25
-    out, lse = c.run(which)
+    out, lse = c.run()
     assert msa.device_status() == msa.MSA_OK
     c.check(out, lse)
 
 
-@pytest.mark.parametrize("which", ["decode", "prefill"])
+@pytest.mark.parametrize("which", FORMS)
 def test_block_scales_far_apart(cuda_ok, which):
-    """Scales of 0, tiny, large and a block whose V alone is large: each block's own scale acts on it."""
-    c = Case(7, ctx=[1300], nq=[2], kv=1, topk=11)
-    for b, (ks, vs) in enumerate([(0.0, 1.0), (1e-20, 1e-20), (2.0 ** -6, 0.0), (2.0 ** -6, 2.0 ** 20), (2.0 ** -5, 2.0 ** -126)]):
+    """Scales of 0, tiny, large, negative and a block whose V alone is large: each block's own scale acts on it."""
+    c = Case(7, ctx=[1300], nq=[2], which=which, kv=1, topk=11)
+    for b, (ks, vs) in enumerate([(0.0, 1.0), (1e-20, 1e-20), (2.0 ** -6, 0.0), (2.0 ** -6, 2.0 ** 20), (2.0 ** -5, 2.0 ** -126),
+                                  (-2.0 ** -6, -2.0 ** -6)]):
         c.ks[c.table[0, b], 0], c.vs[c.table[0, b], 0] = ks, vs
-    out, lse = c.run(which)
+    out, lse = c.run()
     assert msa.device_status() == msa.MSA_OK
     c.check(out, lse)
 
 
-@pytest.mark.parametrize("which", ["decode", "prefill"])
+@pytest.mark.parametrize("which", FORMS)
 def test_nan_reaches_its_own_row_only(cuda_ok, which):
     """A NaN code among a row's keys or values, or in its query, makes that row's heads NaN and no other's."""
-    c = Case(8, ctx=[300, 300, 300, 300], nq=[1] * 4, kv=1, topk=3)
+    c = Case(8, ctx=[300, 300, 300, 300], nq=[1] * 4, which=which, kv=1, topk=3)
     c.k[c.table[0, 1], 0, 5, 7] = 0x7F
     c.v[c.table[1, 0], 0, 9, :] = 0xFF
     c.q[2, 4, 100] = float("nan")
-    out, lse = c.run(which)
+    out, lse = c.run()
     assert msa.device_status() == msa.MSA_OK
     assert out[0].isnan().all() and lse[0].isnan().all() and out[1].isnan().all() and not lse[1].isnan().any()
     assert out[2, 4].isnan().all() and lse[2, 4].isnan() and int(out[2].isnan().sum()) == 128
     c.check(out, lse, [3])
-    ref = Case(8, ctx=[300, 300, 300, 300], nq=[1] * 4, kv=1, topk=3)
-    ro, rl = ref.run(which)
+    ref = Case(8, ctx=[300, 300, 300, 300], nq=[1] * 4, which=which, kv=1, topk=3)
+    ro, rl = ref.run()
     keep = [h for h in range(16) if h != 4]
     assert torch.equal(out[2, keep], ro[2, keep]) and torch.equal(lse[2, keep], rl[2, keep])
 
 
-@pytest.mark.parametrize("which", ["decode", "prefill"])
+@pytest.mark.parametrize("which", FORMS)
+def test_nan_value_behind_a_row_does_not_reach_it(cuda_ok, which):
+    """Rows of one block on both sides of a NaN value: only those that see it are NaN."""
+    c = Case(13, ctx=[100], nq=[100], which=which, kv=1, topk=1)
+    c.v[c.table[0, 0], 0, 60] = 0x7F
+    out, lse = c.run()
+    assert msa.device_status() == msa.MSA_OK
+    assert out[60:100].isnan().all() and not out[:60].isnan().any() and not lse[:100].isnan().any()
+    c.check(out, lse, [*range(0, 60, 7), 59])
+
+
+@pytest.mark.parametrize("which", FORMS)
+def test_every_code_is_read_as_its_value(cuda_ok, which):
+    """One key a row: the output is the value itself, and a one-hot query's lse the key's element."""
+    c = Case(14, ctx=[1] * 16, nq=[1] * 16, which=which, kv=1, topk=1)
+    for s in range(16):
+        codes = (np.arange(128) + 128 * (s // 8)).astype(np.uint8)
+        codes[127] = 0
+        page = c.table[s, 0]
+        c.k[page, 0, 0], c.v[page, 0, 0] = codes, codes
+        c.ks[page, 0], c.vs[page, 0] = 0.5, 0.25
+        c.q[s] = 0
+        for h in range(16):
+            c.q[s, h, 16 * (s % 8) + h] = 1.0
+    out, lse = c.run()
+    assert msa.device_status() == msa.MSA_OK
+    for s in range(16):
+        value = torch.from_numpy(F.decode_bits(c.k[c.table[s, 0], 0, 0]))
+        assert torch.equal(out[s].double().cpu(), (0.25 * value).expand(16, 128))
+        want = 0.5 * value[16 * (s % 8):16 * (s % 8) + 16] / 128 ** 0.5
+        assert torch.allclose(lse[s].double().cpu(), want, rtol=2e-6, atol=1e-6)
+
+
+@pytest.mark.parametrize("which", FORMS)
 def test_bad_pages_and_blocks_are_recorded_and_left_out(cuda_ok, which):
-    c = Case(9, ctx=[2000, 900], nq=[2, 1], kv=2, topk=5, extra_width=1)
+    c = Case(9, ctx=[2000, 900], nq=[2, 1], which=which, kv=2, topk=5, extra_width=1)
     want = c.sel.copy()
     bad_b = int(c.sel[0, 0, 0])
     c.table = c.table.copy()
@@ -210,57 +252,57 @@ def test_bad_pages_and_blocks_are_recorded_and_left_out(cuda_ok, which):
     want[2, 1, 1] = -1
     c.sel[2, 0, 0] = 12                                # a block after the query's
     want[2, 0, 0] = -1
-    c.batch = msa.Batch.make([0, 2, 3], c.ctx, c.table, c.pages)
-    out, lse = c.run(which)
+    c.batch = msa.Batch.make(c.starts.tolist(), c.ctx, c.table, c.pages)
+    out, lse = c.run()
     assert msa.device_status() == msa.MSA_ERR_DEVICE_BOUNDS
     assert msa.device_status() == msa.MSA_OK
     c.sel, c.table = want, good
     c.check(out, lse)
 
 
-@pytest.mark.parametrize("which", ["decode", "prefill"])
+@pytest.mark.parametrize("which", FORMS)
 def test_same_bits_again_on_other_pages_and_another_stream(cuda_ok, which):
-    c = Case(10, ctx=[5000, 260, 3000], nq=[5, 40, 7], topk=16)
-    a = c.run(which)
-    b = c.run(which)
+    c = Case(10, ctx=[5000, 260, 3000], nq=[5, 40, 7], which=which, topk=16)
+    a = c.run()
+    b = c.run()
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
-        e = c.run(which)
+        e = c.run()
     torch.cuda.current_stream().wait_stream(side)
     perm = np.random.default_rng(1).permutation(c.pages)        # page p moves to inv[p]
     inv = np.argsort(perm)
     c.k, c.v, c.ks, c.vs = c.k[perm], c.v[perm], c.ks[perm], c.vs[perm]
     c.table = np.where(c.table >= 0, inv[c.table], -1).astype(np.int32)
-    c.batch = msa.Batch.make([0, 5, 45, 52], c.ctx, c.table, c.pages)
+    c.batch = msa.Batch.make(c.starts.tolist(), c.ctx, c.table, c.pages)
     del c._d
-    f = c.run(which)
+    f = c.run()
     assert msa.device_status() == msa.MSA_OK
     for x in (b, e, f):
         assert torch.equal(a[0], x[0]) and torch.equal(a[1], x[1])
 
 
-@pytest.mark.parametrize("which", ["decode", "prefill"])
+@pytest.mark.parametrize("which", FORMS)
 def test_graphs_with_their_own_workspaces(cuda_ok, which):
     """Two captured calls, replayed in turn and with new inputs in place, give what the eager calls give."""
-    cases = [Case(11, ctx=[2000, 500], nq=[3, 1]), Case(12, ctx=[129, 4000], nq=[9, 30])]
+    cases = [Case(11, ctx=[2000, 500], nq=[3, 1], which=which), Case(12, ctx=[129, 4000], nq=[9, 30], which=which)]
     graphs, results = [], []
     for c in cases:
-        c.run(which)                                             # the first call is not captured
+        c.run()                                             # the first call is not captured
         d = c.device()
         out, lse = torch.zeros_like(d[0]), torch.zeros(d[0].shape[:2], device="cuda")
-        ws = torch.zeros(WORKSPACE[which](c.cfg, c.batch), dtype=torch.uint8, device="cuda")
+        ws = torch.zeros(c.size(c.cfg, c.batch), dtype=torch.uint8, device="cuda")
         torch.cuda.synchronize()
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
-            ATTN[which](c.cfg, c.batch, *d, out, lse, ws)
+            c.fn(c.cfg, c.batch, *d, out, lse, ws)
         graphs.append(g)
         results.append((out, lse, ws))
     for turn in range(3):
         for c, g, (out, lse, _) in zip(cases, graphs, results):
             c.device()[0].mul_(0.5 if turn else 1.0)
             g.replay()
-            want = c.run(which)
+            want = c.run()
             assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
     assert msa.device_status() == msa.MSA_OK
 
