@@ -94,6 +94,28 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// two fp32 operations an instruction (the same roundings)
+__device__ __forceinline__ unsigned long long pair(float a, float b) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(unsigned long long v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 // Instruction descriptor, kind::f16: f16 x f16 -> fp32
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
@@ -656,6 +678,7 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
       const float mc = (m > -INFINITY) ? m * sc : 0.f;   // -inf only on rows past the tile's entries
       // ---- P = exp2(scale * S - max) as f16 pairs into P[w] (TMEM), two halves of 64 keys
       float l0 = 0.f, l1 = 0.f;
+      const unsigned long long sc2 = pair(sc, sc), mc2 = pair(-mc, -mc);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         uint32_t pk[32];
@@ -664,7 +687,10 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
           const int c = half * 64 + q2 * 2;
           const float x0 = c < 32 ? v0[c] : c < 64 ? v1[c - 32] : c < 96 ? v2[c - 64] : v3[c - 96];
           const float x1 = c + 1 < 32 ? v0[c + 1] : c + 1 < 64 ? v1[c - 31] : c + 1 < 96 ? v2[c - 63] : v3[c - 95];
-          const float p0 = exp2f(fmaf(x0, sc, -mc)), p1 = exp2f(fmaf(x1, sc, -mc));   // exp2(-inf) = 0
+          float p0, p1;
+          unpair(fma2(pair(x0, x1), sc2, mc2), p0, p1);
+          p0 = exp2f(p0);                          // exp2(-inf) = 0
+          p1 = exp2f(p1);
           if (q2 & 1) l1 += p0 + p1; else l0 += p0 + p1;
           pk[q2] = pack_f16(p0, p1);
         }
@@ -694,15 +720,21 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
       // a NaN among the V rows that this row sees (the converters took it out)
       const int4 vn = *reinterpret_cast<const int4*>(s_vnan[(nbuckets - 1) & 3]);
       const float inv = min(min(vn.x, vn.y), min(vn.z, vn.w)) < vis ? __uint_as_float(0x7FC00000u) : rec.vs / l;
+      const unsigned long long inv2 = pair(inv, inv);
+      float y0, y1;
 #pragma unroll
       for (int q8 = 0; q8 < 16; ++q8) {
         const int col = q8 * 8;                   // output dims col .. col+7
         const float* ov = q8 < 4 ? o0 + col : q8 < 8 ? o1 + col - 32 : q8 < 12 ? o2 + col - 64 : o3 + col - 96;
         uint4 wv;
-        wv.x = pack_bf16(ov[0] * inv, ov[1] * inv);
-        wv.y = pack_bf16(ov[2] * inv, ov[3] * inv);
-        wv.z = pack_bf16(ov[4] * inv, ov[5] * inv);
-        wv.w = pack_bf16(ov[6] * inv, ov[7] * inv);
+        unpair(mul2(pair(ov[0], ov[1]), inv2), y0, y1);
+        wv.x = pack_bf16(y0, y1);
+        unpair(mul2(pair(ov[2], ov[3]), inv2), y0, y1);
+        wv.y = pack_bf16(y0, y1);
+        unpair(mul2(pair(ov[4], ov[5]), inv2), y0, y1);
+        wv.z = pack_bf16(y0, y1);
+        unpair(mul2(pair(ov[6], ov[7]), inv2), y0, y1);
+        wv.w = pack_bf16(y0, y1);
         *reinterpret_cast<uint4*>(stage + (col >> 6) * 16384 + sw128_offset(r, (col & 63) * 2)) = wv;
       }
       if (valid)
