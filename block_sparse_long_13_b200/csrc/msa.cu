@@ -822,12 +822,19 @@ msa_status_t make_code_map(CUtensorMap* m, const void* cache, const msa_config_t
 struct PrefillFp8Ws {
   size_t counts, bases, tile_rec, part_lse, part_o, bytes;
   int64_t entries, nbuckets, max_tiles;
+  int win_shift, win_buckets;
 };
 
 // The entries' buckets and ranks lie where the partials come later (256 x 16 bytes an entry).
 PrefillFp8Ws prefill_fp8_plan(const msa_config_t* c, const msa_batch_t* b) {
   PrefillFp8Ws w{};
-  w.nbuckets = static_cast<int64_t>(b->num_seqs) * c->num_kv_heads * b->max_blocks_per_seq;
+  // windows of 8192 rows, or of more where their counters would pass 2^22 (32 MiB of them)
+  const int64_t plain = static_cast<int64_t>(b->num_seqs) * c->num_kv_heads * b->max_blocks_per_seq;
+  auto windows = [&] { return std::max<int64_t>(1, (static_cast<int64_t>(b->total_q) + (1LL << w.win_shift) - 1) >> w.win_shift); };
+  w.win_shift = 13;
+  while (w.win_shift < 25 && plain * windows() > (1LL << 22)) ++w.win_shift;   // total_q < 2^25: one window at the end
+  w.win_buckets = static_cast<int>(std::min<int64_t>(plain, 0x7FFFFFFF));
+  w.nbuckets = plain * windows();
   w.entries = static_cast<int64_t>(b->total_q) * c->num_kv_heads * c->topk;
   w.max_tiles = (w.entries + msa::ATTP_TOK - 1) / msa::ATTP_TOK + std::min(w.nbuckets, w.entries);
   size_t o = 0;
@@ -959,6 +966,8 @@ msa_status_t msa_attn_prefill_fp8(const msa_config_t* cfg, const msa_batch_t* ba
   s.topk = k;
   s.max_blocks = batch->max_blocks_per_seq;
   s.nbuckets = static_cast<int>(w.nbuckets);
+  s.win_shift = w.win_shift;
+  s.win_buckets = w.win_buckets;
   s.num_pages = batch->num_pages;
   s.max_tiles = static_cast<int>(w.max_tiles);
   // few rows: eight to a CTA, so that its chain of look-ups is short; many: 32, so that hot blocks take fewer atomics

@@ -138,6 +138,14 @@ def test_attention_matches_oracle(cuda_ok, shape, which):
     c.check(out, lse)
 
 
+def test_more_rows_than_a_window(cuda_ok):
+    """Rows of several scheduling windows, tiles in several rounds over the CTAs."""
+    c = Case(15, ctx=[9000, 12000, 100], nq=[8000, 9500, 50], which="prefill", kv=1, topk=12)
+    out, lse = c.run()
+    assert msa.device_status() == msa.MSA_OK
+    c.check(out, lse, [*range(0, c.rows, 251), 7999, 8000, 8191, 8192, 16383, 16384, 17499, 17500, 17549])
+
+
 @pytest.mark.parametrize("which", FORMS)
 def test_rows_without_keys_and_padded_rows(cuda_ok, which):
     """A selection of -1 only gives out 0 and lse -inf; rows behind the last sequence stay as they were."""
