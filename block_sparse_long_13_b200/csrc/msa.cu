@@ -887,14 +887,16 @@ msa_status_t run_decode_fp8(const msa_config_t* cfg, const msa_batch_t* batch, c
   return MSA_OK;
 }
 
-// Which form a prefill call takes.  The tiles' schedule, launches and merge cost about 40 us before the first tile;
-// the slots cost 0.65 us a block and CTA, and about six blocks' time more a (row, group).  Measured, us, slots / tiles:
-// 16 blocks a row, 4 groups: 128 rows 46 / 70 and 45 / 62 (32K and 4K contexts), 256 rows 81 / 94 and 81 / 89, 512 rows
-// 151 / 146 and 151 / 119; 4 blocks a row, one group: 1024 rows 34 / 42, 2048 rows 63 / 57; one block a row, 4 groups:
-// 1024 rows 64 / 54.
+// Which form a prefill call takes.  The slots take about 9.5 us + 4.4 ns a slot + 9 ns a (row, group), the tiles 23 us +
+// 2.6 ns a slot + 20 ns a bucket (its codes are widened, its last tile is not full); the page table's width stands for
+// the buckets of a sequence, so a cap keeps a table much wider than the contexts from deciding.  Measured, us, slots /
+// tiles, 16 blocks a row and 4 groups: 64 rows of a 32K context 26 / 53, 192 rows 63 / 75, 256 rows 80 / 84, 512 rows 150 /
+// 125; 128 rows of a 4K context 44 / 50, 256 rows 80 / 72; 8 x 32 rows of 8K contexts 77 / 129; 4 blocks a row, one group:
+// 512 rows 21 / 29, 2048 rows 62 / 47; one block a row, one group: 1024 rows 21 / 27, 2048 rows 36 / 33.
 bool few_slots(const msa_config_t* c, const msa_batch_t* b) {
-  const int64_t units = static_cast<int64_t>(b->total_q) * c->num_kv_heads;
-  return units * (c->topk + 10) <= 27000;
+  const int64_t units = static_cast<int64_t>(b->total_q) * c->num_kv_heads, slots = units * c->topk;
+  const int64_t buckets = std::min(slots, static_cast<int64_t>(b->num_seqs) * c->num_kv_heads * b->max_blocks_per_seq);
+  return slots + 5 * units <= std::min<int64_t>(24576, 8000 + 12 * buckets);
 }
 
 // theta^(-2i/r) / (2 pi) turns of the rotation pairs, modulo 1, as multiples of 2^-64
