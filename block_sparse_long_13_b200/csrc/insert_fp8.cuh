@@ -159,9 +159,10 @@ __device__ __forceinline__ void kv_insert_piece(const KvInsertArgs& a, const Rop
     kmax = fmaxf(kmax, s_max[0][w]);
     vmax = fmaxf(vmax, s_max[1][w]);
   }
-  // a scale that is not positive holds nothing: it counts as 0
-  const bool k_grown = slot0 == 0 || !(k_old > 0.f) || kmax > E4M3_MAX * k_old;
-  const bool v_grown = slot0 == 0 || !(v_old > 0.f) || vmax > E4M3_MAX * v_old;
+  // a scale that is not a positive number holds nothing: it counts as 0
+  const bool k_held = k_old > 0.f && k_old < INFINITY, v_held = v_old > 0.f && v_old < INFINITY;
+  const bool k_grown = slot0 == 0 || !k_held || kmax > E4M3_MAX * k_old;
+  const bool v_grown = slot0 == 0 || !v_held || vmax > E4M3_MAX * v_old;
   const float ks = k_grown ? e4m3_block_scale(kmax) : k_old, vs = v_grown ? e4m3_block_scale(vmax) : v_old;
   // a power of two's reciprocal is exact, and so is a product with it; other scales (a cache that something else wrote)
   // are divided by
@@ -188,8 +189,8 @@ __device__ __forceinline__ void kv_insert_piece(const KvInsertArgs& a, const Rop
     *reinterpret_cast<uint2*>(vt + (slot0 + r) * QKR_D + 8 * hl) =
         make_uint2(e4m3x4_of(z[0], z[1], z[2], z[3]), e4m3x4_of(z[4], z[5], z[6], z[7]));
   }
-  if (slot0 > 0 && k_grown) rescale_codes(kt, slot0, k_old > 0.f ? __fdiv_rn(k_old, ks) : 0.f);
-  if (slot0 > 0 && v_grown) rescale_codes(vt, slot0, v_old > 0.f ? __fdiv_rn(v_old, vs) : 0.f);
+  if (slot0 > 0 && k_grown) rescale_codes(kt, slot0, k_held ? __fdiv_rn(k_old, ks) : 0.f);
+  if (slot0 > 0 && v_grown) rescale_codes(vt, slot0, v_held ? __fdiv_rn(v_old, vs) : 0.f);
   if (tid == 0) {
     if (k_grown) a.k_scale[tile] = ks;
     if (v_grown) a.v_scale[tile] = vs;

@@ -944,6 +944,7 @@ msa_status_t msa_attn_prefill_fp8(const msa_config_t* cfg, const msa_batch_t* ba
   if (st != MSA_OK) return st;
   const PrefillFp8Ws w = prefill_fp8_plan(cfg, batch);
   CHECK_SUP(w.nbuckets < (1L << 31) - 1024 && w.max_tiles < (1L << 31), "too many (sequence, group, block) buckets");
+  CHECK_SUP(w.entries * 16 < (1LL << 31), "too many (row, head, slot) partials");
   if (batch->total_q == 0) return MSA_OK;
   if (few_slots(cfg, batch))
     return run_decode_fp8(cfg, batch, q, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale, block_idx, out, lse, workspace, stream);

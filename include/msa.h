@@ -310,7 +310,8 @@ msa_status_t msa_attn_prefill_fp8(const msa_config_t* cfg, const msa_batch_t* ba
  *                           e4m3(code * old / new): exact for codes that stay normal
  *                           where the old scale is a power of two
  *   code = e4m3(clamp(value / scale, -448, 448)), nearest even; infinities
- *   saturate, NaN stays NaN.  An old scale that is not positive counts as 0.
+ *   saturate, NaN stays NaN.  An old scale that is not a positive, normal and finite
+ *   number counts as 0 (the page's earlier codes become 0).
  * Slots behind the last new row, and other pages, are left as they were, and so
  * are the q_out rows t >= q_start[num_seqs] of a padded batch.  The sequences of
  * a call must not write to a common page, and k_new / v_new must not overlap

@@ -101,7 +101,7 @@ def insert(q, k_new, v_new, q_w, k_w, seq, pos, page_table, k_codes, v_codes, k_
                 y = np.stack([x[t, g] for t in ts])
                 a = float(np.max(np.where(np.isfinite(y), np.abs(y), 0.0)))
                 old = float(new_scale[page, g])
-                held = old if old > 0 else 0.0
+                held = old if 0 < old < np.inf else 0.0
                 grown = first == 0 or held == 0.0 or a > E4M3_MAX * held
                 s = block_scale(a) if grown else old
                 if grown and first > 0:

@@ -148,6 +148,29 @@ def test_binding_refuses_wrong_shapes_and_cpu_tensors(lib):
     assert "CUDA tensor" in _refused(msa.advance_batch, *adv.values())
 
 
+def test_binding_refuses_another_device(lib, monkeypatch):
+    """A tensor that is not on the current device is named, whatever else is right."""
+    class On:
+        shape, dtype, is_cuda = torch.Size([4]), torch.int32, True
+
+        def __init__(self, device):
+            self.device = device
+
+        def get_device(self):
+            return self.device
+
+        def is_contiguous(self):
+            return True
+
+        def data_ptr(self):
+            return 16
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    assert msa._pointers((On(0), torch.int32, (4,), "a"), (None, torch.int32, (4,), "b")) == [16, 0]
+    assert "b is on device 1, but device 0 is current" in _refused(msa._pointers, (On(0), torch.int32, (4,), "a"),
+                                                                  (On(1), torch.int32, (4,), "b"))
+
+
 # ----------------------------------------------------------------- the oracle
 def test_block_scale_is_the_least_power_of_two_that_holds_the_value():
     assert K.block_scale(448.0) == 1.0 and K.block_scale(np.nextafter(448.0, 500.0)) == 2.0

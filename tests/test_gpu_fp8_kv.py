@@ -171,6 +171,15 @@ def test_holes_and_order_of_the_selection_do_not_matter(cuda_ok, which):
 
 
 @pytest.mark.parametrize("which", FORMS)
+def test_a_block_selected_twice_counts_twice(cuda_ok, which):
+    c = Case(16, ctx=[700, 500], nq=[2, 3], which=which, kv=2, topk=5)
+    c.sel[:c.main, :, 0] = c.sel[:c.main, :, 1]
+    out, lse = c.run()
+    assert msa.device_status() == msa.MSA_OK
+    c.check(out, lse)
+
+
+@pytest.mark.parametrize("which", FORMS)
 @pytest.mark.parametrize("q_size", [1e-30, 1e-3, 4.0])
 def test_query_sizes(cuda_ok, which, q_size):
     """Queries from tiny to large, a head of zeros, elements 2^-12 below their head's largest."""
@@ -421,6 +430,21 @@ def test_insert_scales_at_their_borders(cuda_ok):
     assert msa.device_status() == msa.MSA_OK
 
 
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), -1.0, 1e-42])
+def test_insert_where_the_old_scale_holds_nothing(cuda_ok, scale):
+    """A scale that is no positive number (a denormal one counts as 0): the page's earlier codes become 0."""
+    c = _insert_case(27, ctx=[40, 77], nq=[4, 2], kv=1)
+    page = int(c["table"][0, 0])
+    for s in c["scales"]:
+        s[page] = scale
+    got = _insert(c)
+    assert msa.device_status() == msa.MSA_OK
+    for codes, scales, new in ((got[1], got[3], c["k_new"]), (got[2], got[4], c["v_new"])):
+        assert not (codes[page, 0, :36] & 0x7F).any() and (codes[page, 0, 36:40] & 0x7F).any()
+        assert 448 * float(scales[page, 0]) >= 1e-3 and np.isfinite(float(scales[page, 0]))
+    assert float(got[4][page, 0]) == K.block_scale(float(c["v_new"][:4].abs().max()))
+
+
 def test_insert_of_infinities_and_nan(cuda_ok):
     """An infinity saturates and a NaN stays NaN; neither moves the page's scale."""
     c = _insert_case(24, ctx=[40], nq=[4], kv=1)
@@ -587,6 +611,74 @@ def test_advance_steps_conserve_the_pages(cuda_ok):
 
 
 # ----------------------------------------------------------------- together
+def test_a_captured_decode_step(cuda_ok):
+    """advance, insert and attention of a decode step as one graph, replayed over page borders: what the calls one by one
+    give, bit for bit."""
+    rng = np.random.default_rng(8)
+    kv, topk, width, n = 2, 4, 4, 5
+    pages = n * width
+    cfg = msa.Config(num_q_heads=16 * kv, num_kv_heads=kv, idx_heads=kv, topk=topk)
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    host = [126, 127, 128, 255, 1]
+    table = np.full((n, width), -1)
+    perm, at = rng.permutation(pages), 0
+    for s, c in enumerate(host):
+        for b in range(-(-c // 128)):
+            table[s, b] = perm[at]
+            at += 1
+
+    def state():
+        ring = [-1] * pages
+        for i, p in enumerate(perm[at:].tolist()):
+            ring[(pages - 2 + i) % pages] = p
+        st = dict(ctx=dev(host), pool=dev([pages - 2, pages - at, 0, 0]), ring=dev(ring), table=dev(table.tolist()),
+                  q_start=dev([0] * (n + 1)), slots=dev([0] * n), delta=dev([1] * n))
+        g = torch.Generator(device="cuda").manual_seed(3)
+        st["kc"], st["vc"] = (torch.randint(0, 127, (pages, kv, 128, 128), dtype=torch.uint8, device="cuda", generator=g) for _ in range(2))
+        st["ks"], st["vs"] = (torch.full((pages, kv), 2.0 ** -8, device="cuda") for _ in range(2))
+        st["q"], st["kn"], st["vn"] = (torch.zeros(n, h, 128, dtype=torch.bfloat16, device="cuda") for h in (16 * kv, kv, kv))
+        st["qo"], st["out"] = torch.empty_like(st["q"]), torch.empty_like(st["q"])
+        st["lse"] = torch.empty(n, 16 * kv, device="cuda")
+        st["sel"] = torch.full((n, kv, topk), -1, dtype=torch.int32, device="cuda")
+        st["batch"] = msa.Batch(q_start=st["q_start"], ctx_len=st["ctx"], page_table=st["table"], total_q=n, max_q_per_seq=1,
+                                num_pages=pages)
+        st["ws"] = torch.empty(msa.decode_fp8_workspace_bytes(cfg, st["batch"]), dtype=torch.uint8, device="cuda")
+        return st
+
+    weight = torch.ones(128, dtype=torch.bfloat16, device="cuda")
+
+    def step(st):
+        msa.advance_batch(st["delta"], st["ctx"], st["table"], st["ring"], st["pool"], st["ctx"], st["pool"], st["q_start"], st["slots"])
+        msa.qknorm_rope_insert_fp8(cfg, st["batch"], st["q"], st["kn"], st["vn"], weight, weight, st["qo"], st["kc"], st["vc"], st["ks"], st["vs"])
+        msa.attn_decode_fp8(cfg, st["batch"], st["qo"], st["kc"], st["vc"], st["ks"], st["vs"], st["sel"], st["out"], st["lse"], st["ws"])
+
+    def feed(st, turn):
+        g = torch.Generator(device="cuda").manual_seed(100 + turn)
+        for name in ("q", "kn", "vn"):
+            st[name].copy_(torch.randn(st[name].shape, generator=g, device="cuda"))
+        for s, c in enumerate(host):
+            cur = (c + turn) // 128
+            st["sel"][s, :, :cur + 1] = torch.arange(cur + 1, dtype=torch.int32, device="cuda")
+
+    a, b = state(), state()
+    warm = state()
+    feed(warm, 0)
+    step(warm)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(a)
+    for turn in range(5):
+        feed(a, turn)
+        feed(b, turn)
+        graph.replay()
+        step(b)
+        for name in ("out", "lse", "kc", "vc", "ks", "vs", "ctx", "pool", "table", "ring", "slots"):
+            assert torch.equal(a[name], b[name]), (turn, name)
+    assert msa.device_status() == msa.MSA_OK and a["pool"].tolist()[2] == 0
+    assert a["ctx"].tolist() == [c + 5 for c in host]
+
+
 def test_a_served_batch_step_by_step(cuda_ok):
     """advance -> insert -> attention over a prefill, a mixed chunk, decode steps and a rollback, with every block
     selected: the attention is the dense causal one over the tokens that the cache holds."""
