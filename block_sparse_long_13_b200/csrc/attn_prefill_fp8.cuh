@@ -129,8 +129,9 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) 
 // those of 16,384 rows do not (the last 128K chunk 2.94 ms without windows, 2.84 with, 2.93 with 4096 rows).  Three kernels turn the
 // entries into tiles of up to 8 of a bucket:
 //   count  every entry's bucket and rank in it (a counter per bucket)
-//   bases  every bucket's run of tiles, ceil(count / 8) of them
-//   place  every entry to tile base + rank / 8, place rank % 8; the first of a tile writes the tile's head
+//   bases  every bucket's run of tiles, ceil(count / 8) of them, and its stretch of cost
+//   place  every entry to tile base + rank / 8, place rank % 8; the first of a tile writes the tile's head, and the
+//          tile as the first one of the CTAs whose share of the cost begins in it
 // The counters' order decides which entries share a tile and where it stands, which no result depends on: an entry's
 // rows of the products are its own.
 struct SchedFp8Args {
@@ -140,12 +141,14 @@ struct SchedFp8Args {
   const int32_t* page_table;
   const float* k_scale;       // [pages][Hkv]
   const float* v_scale;
-  int* counts;                // [nbuckets], then the number of tiles; zeroed
-  int* bases;                 // [nbuckets]
+  unsigned long long* total;  // cost << 32 | number of tiles, zeroed with the counts behind it
+  int* counts;                // [nbuckets]
+  unsigned long long* bases;  // [nbuckets]: first cost << 32 | first tile
+  int* starts;                // [ctas]: first tile of a CTA's share of the cost
   int2* entries;              // [total_q * Hkv * topk]: bucket (-1: none), rank
   int4* tile_rec;             // [max_tiles][4]: one 64-byte record per tile
   float* part_lse;            // [total_q][Hq][topk]
-  int num_seqs, total_q, Hq, Hkv, topk, max_blocks, nbuckets, num_pages, max_tiles, cta_rows;
+  int num_seqs, total_q, Hq, Hkv, topk, max_blocks, nbuckets, num_pages, max_tiles, cta_rows, ctas;
   int win_shift, win_buckets; // rows of a window (log2) and its buckets
 };
 
@@ -223,35 +226,40 @@ __global__ void __launch_bounds__(256) sched_fp8_count_kernel(const SchedFp8Args
   }
 }
 
-// CTA = 1024 buckets, thread = 4: their tiles' exclusive sums over the CTA, whose run begins where the number of tiles
+// A tile's time is two units of cost; a change of bucket (its K to be widened, the pipeline to be filled again) is
+// SCH8_CHANGE more.
+constexpr int SCH8_CHANGE = 1;
+
+// CTA = 1024 buckets, thread = 4: their exclusive sums of cost and tiles over the CTA, whose run begins where the totals
 // stood.
 __global__ void __launch_bounds__(256) sched_fp8_bases_kernel(const SchedFp8Args a) {
-  __shared__ int s_w[8], s_base;
+  __shared__ unsigned long long s_w[8], s_base;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_launch_dependents();
   pdl_wait();
   const int i0 = (blockIdx.x * 256 + tid) * 4;
-  int tl[4], sum = 0;
+  unsigned long long tl[4], sum = 0;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    tl[k] = i0 + k < a.nbuckets ? (a.counts[i0 + k] + ATTP_TOK - 1) / ATTP_TOK : 0;
+    const int n = i0 + k < a.nbuckets ? (a.counts[i0 + k] + ATTP_TOK - 1) / ATTP_TOK : 0;
+    tl[k] = n ? static_cast<unsigned long long>(2 * n + SCH8_CHANGE) << 32 | n : 0ull;
     sum += tl[k];
   }
-  int v = sum;
+  unsigned long long v = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int n = __shfl_up_sync(0xFFFFFFFFu, v, o);
+    const unsigned long long n = __shfl_up_sync(0xFFFFFFFFu, v, o);
     if (lane >= o) v += n;
   }
   if (lane == 31) s_w[warp] = v;
   __syncthreads();
   if (tid == 0) {
-    int total = 0;
-    for (int w = 0; w < 8; ++w) { const int n = s_w[w]; s_w[w] = total; total += n; }
-    s_base = total ? atomicAdd(a.counts + a.nbuckets, total) : 0;
+    unsigned long long total = 0;
+    for (int w = 0; w < 8; ++w) { const unsigned long long n = s_w[w]; s_w[w] = total; total += n; }
+    s_base = total ? atomicAdd(a.total, total) : 0ull;
   }
   __syncthreads();
-  int at = s_base + s_w[warp] + v - sum;
+  unsigned long long at = s_base + s_w[warp] + v - sum;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     if (i0 + k < a.nbuckets) a.bases[i0 + k] = at;
@@ -272,10 +280,16 @@ __global__ void __launch_bounds__(256) sched_fp8_place_kernel(const SchedFp8Args
   const int2 x = a.entries[e];
   if (x.x < 0) return;
   const int t = static_cast<int>(e / per_row), slot = static_cast<int>(e % a.topk);
-  int4* r = a.tile_rec + static_cast<long>(a.bases[x.x] + x.y / ATTP_TOK) * 4;
-  const int place = x.y % ATTP_TOK;
+  const unsigned long long base = a.bases[x.x];
+  const int k = x.y / ATTP_TOK, tile = static_cast<int>(base & 0xFFFFFFFFu) + k, place = x.y % ATTP_TOK;
+  int4* r = a.tile_rec + static_cast<long>(tile) * 4;
   reinterpret_cast<int*>(r + 2)[place] = (t << 6) | slot;
   if (place != 0) return;
+  // CTA c's share begins at cost total c / ctas
+  const unsigned long long total = *a.total >> 32, first = base >> 32;
+  const unsigned long long from = k ? first + SCH8_CHANGE + 2 * k : first, to = first + SCH8_CHANGE + 2 * k + 2;
+  const int c1 = static_cast<int>(min(static_cast<unsigned long long>(a.ctas), (to * a.ctas + total - 1) / total));
+  for (int c = static_cast<int>((from * a.ctas + total - 1) / total); c < c1; ++c) a.starts[c] = tile;
   const int n = min(ATTP_TOK, a.counts[x.x] - x.y);
   const int y = x.x % a.win_buckets;
   const int b = y % a.max_blocks, g = (y / a.max_blocks) % a.Hkv, seq = y / (a.max_blocks * a.Hkv);
@@ -289,11 +303,12 @@ __global__ void __launch_bounds__(256) sched_fp8_place_kernel(const SchedFp8Args
 // ------------------------------------------------------------------ tiles
 struct AttnPrefillFp8Args {
   const int4* tile_rec;      // [tiles][4] records written by sched_fp8_place_kernel
-  const int* total_tiles;
+  const unsigned long long* total;   // cost << 32 | number of tiles
+  const int* starts;         // [gridDim.x]
   const uint8_t* k_cache;    // [pages][Hkv][128][128] codes
   const uint8_t* v_cache;
   float* part_lse;           // [total_q][Hq][topk]
-  int Hq, topk, max_tiles;
+  int Hq, topk;
   float scale_log2;
 };
 
@@ -347,21 +362,20 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
   tc_fence_after();
   const uint32_t tmem = s_tmem;
 
-  pdl_launch_dependents();
   pdl_wait();                                            // the records
   // Tiles come by bucket.  All CTAs move through the list together, ATP8_RUN tiles each and round, so that they gather
-  // from the same window and group; a short list is cut into one run per CTA instead, so that a bucket's tiles stay
-  // together (runs of 32: mixed chunks 302 us instead of 269).
-  const int T = min(*a.total_tiles, a.max_tiles);
+  // from the same window and group.  A short list is cut into one run per CTA instead, so that a bucket's tiles stay
+  // together (runs of 32: mixed chunks 302 us instead of 269), at equal shares of the cost (equal numbers of tiles left
+  // the SMs idle for a quarter of the time).
+  const int T = static_cast<int>(*a.total & 0xFFFFFFFFu);
   const int G = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
   const bool shortlist = T <= 2 * G * ATP8_RUN;
-  const int run = shortlist ? (T + G - 1) / G : ATP8_RUN;
-  const int full = shortlist ? 0 : T / (G * run);           // whole rounds
-  const int ntile = full * run + max(0, min(run, T - full * G * run - c * run));
+  const int full = T / (G * ATP8_RUN);                      // whole rounds
+  const int start = shortlist ? (T ? a.starts[c] : 0) : c * ATP8_RUN;
+  const int ntile = shortlist ? (T ? (c + 1 < G ? a.starts[c + 1] : T) - start : 0)
+                              : full * ATP8_RUN + max(0, min(ATP8_RUN, T - full * G * ATP8_RUN - start));
   // global tile of this CTA's i-th tile
-  auto tile_of = [=](int i) -> int {
-    return shortlist ? c * run + i : (i / ATP8_RUN) * (G * ATP8_RUN) + c * ATP8_RUN + i % ATP8_RUN;
-  };
+  auto tile_of = [=](int i) -> int { return shortlist ? start + i : (i / ATP8_RUN) * (G * ATP8_RUN) + start + i % ATP8_RUN; };
 
   if (warp < 4) {
   regs_dec<ATP8_REGS_CTRL>();
@@ -774,7 +788,6 @@ struct MergeFp8Args {
 __global__ void __launch_bounds__(256) attn_merge_fp8_kernel(const MergeFp8Args a) {
   __shared__ float s_w[ATTP_G][MRG_MAXK];   // per head and slot: exp(lse - max), or -1 (no partial)
   const int t = blockIdx.x / a.Hkv, g = blockIdx.x % a.Hkv;
-  pdl_wait();                               // the partials
   if (t >= __ldg(a.q_start + a.num_seqs)) return;
   const int h = threadIdx.x >> 4, d8 = threadIdx.x & 15;
   const int head = g * ATTP_G + h;
