@@ -21,6 +21,7 @@ namespace msa {
 // Warpgroup 0: producer and issuer warps; 1: converters; 2, 3: softmax.  Register split (setmaxnreg) of the launch's
 // 128 a thread: 128 * (56 + 88 + 184 + 184) = 65536.
 constexpr int ATP8_THREADS = 512;
+constexpr int ATP8_RECS = 8;     // ring of records
 constexpr int ATP8_RUN = 64;      // tiles of a CTA and round
 constexpr int ATP8_REGS_CTRL = 56, ATP8_REGS_CONV = 88, ATP8_REGS_SOFTMAX = 184;
 static_assert(ATP8_REGS_CTRL + ATP8_REGS_CONV + 2 * ATP8_REGS_SOFTMAX <= 4 * 128, "register split exceeds the launch");
@@ -147,7 +148,7 @@ struct SchedFp8Args {
   int* starts;                // [ctas]: first tile of a CTA's share of the cost
   int2* entries;              // [total_q * Hkv * topk]: bucket (-1: none), rank
   int4* tile_rec;             // [max_tiles][4]: one 64-byte record per tile
-  float* part_lse;            // [total_q][Hq][topk]
+  float2* part_lse;           // [total_q][Hkv][topk][16 heads], see AttnPrefillFp8Args
   int num_seqs, total_q, Hq, Hkv, topk, max_blocks, nbuckets, num_pages, max_tiles, cta_rows, ctas;
   int win_shift, win_buckets; // rows of a window (log2) and its buckets
 };
@@ -180,7 +181,8 @@ __global__ void __launch_bounds__(256) sched_fp8_count_kernel(const SchedFp8Args
     if (b < a.max_blocks && b * 128 <= p) page = __ldg(a.page_table + static_cast<long>(s) * a.max_blocks + b);
     if (page < 0 || page >= a.num_pages) {
       flag_error(MSA_DEV_BOUNDS);
-      for (int h = 0; h < ATTP_G; ++h) a.part_lse[(static_cast<long>(t) * a.Hq + g * ATTP_G + h) * a.topk + slot] = -INFINITY;
+      float2* pl = a.part_lse + ((static_cast<long>(t) * a.Hkv + g) * a.topk + slot) * ATTP_G;
+      for (int h = 0; h < ATTP_G; ++h) pl[h] = make_float2(-INFINITY, 0.f);
       return -1;
     }
     return (t >> a.win_shift) * a.win_buckets + (s * a.Hkv + g) * a.max_blocks + b;
@@ -301,34 +303,44 @@ __global__ void __launch_bounds__(256) sched_fp8_place_kernel(const SchedFp8Args
 }
 
 // ------------------------------------------------------------------ tiles
+// bulk_store with an L2 policy
+__device__ __forceinline__ void bulk_store_hint(void* dst, const void* src, uint32_t bytes, uint64_t policy) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group.L2::cache_hint [%0], [%1], %2, %3;"
+               ::"l"(reinterpret_cast<uint64_t>(dst)), "r"(smem_u32(src)), "r"(bytes), "l"(policy)
+               : "memory");
+}
+
 struct AttnPrefillFp8Args {
   const int4* tile_rec;      // [tiles][4] records written by sched_fp8_place_kernel
   const unsigned long long* total;   // cost << 32 | number of tiles
   const int* starts;         // [gridDim.x]
   const uint8_t* k_cache;    // [pages][Hkv][128][128] codes
   const uint8_t* v_cache;
-  float* part_lse;           // [total_q][Hq][topk]
-  int Hq, topk;
+  // Partials of (row, group, slot): O is not divided by l and counts codes, [16 pieces of 8 dims][16 heads][8], 4 KiB that one
+  // bulk copy stores; of each head log2(sum) and v_scale / l, the factor that O still wants.
+  __nv_bfloat16* part_o;     // [total_q][Hkv][topk][2048]
+  float2* part_lse;          // [total_q][Hkv][topk][16 heads]
+  int Hq, Hkv, topk;
   float scale_log2;
 };
 
 __global__ void __launch_bounds__(ATP8_THREADS, 1)
 attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as [total_q*Hq][128]
-                        const __grid_constant__ CUtensorMap tmap_po,    // partial O as [total_q*topk*Hq][128]
                         const AttnPrefillFp8Args a) {
   extern __shared__ __align__(1024) uint8_t dsmem[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~uintptr_t(1023));
   uint8_t* q_s = smem;                                  // 3 x 32 KiB: [half][128 rows][64]
   uint8_t* k_s = q_s + ATTP_QBUF * ATTP_QBYTES;         // [half][128 keys][64]
   uint8_t* v_s = k_s + ATTP_KVBYTES;                    // [half][128 keys][64]
-  uint8_t* o_s = v_s + ATTP_KVBYTES;                    // 2 x 32 KiB: [half][128 rows][64 dims]
+  uint8_t* o_s = v_s + ATTP_KVBYTES;                    // 2 x 32 KiB: [8 entries][16 pieces][16 heads][8 dims]
 
   // Per warpgroup w (its own tile sequence, so a parity never runs two phases ahead): s_full[w] S is in
   // TMEM, p_full[w] P is in TMEM (one arrival per warp), o_full[w] O[w] holds its tile, o_empty[w] O[w]
   // has been read (one arrival per warp).  k_full, v_full: a bucket's tile is widened (one arrival per converter
   // warp); k_empty, v_empty: its last S, its last P V is done.
   __shared__ uint64_t k_full, k_empty, v_full, v_empty, q_full[ATTP_QBUF], q_empty[ATTP_QBUF], s_full[2], p_full[2], o_full[2],
-      o_empty[2], drain_bar;
+      o_empty[2], rec_full[ATP8_RECS], drain_bar;
+  __shared__ int4 s_rec[ATP8_RECS][4];            // the softmax warps' records (the first field: which bucket of this CTA's)
   __shared__ __align__(16) int s_vnan[4][4];      // per bucket (a ring) and converter warp: its first V row with a NaN code, or 128
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
@@ -350,6 +362,7 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
       mbar_init(&o_full[i], 1);
       mbar_init(&o_empty[i], 4);
     }
+    for (int i = 0; i < ATP8_RECS; ++i) mbar_init(&rec_full[i], 1);
     mbar_init(&drain_bar, 1);
     fence_mbar_init();
   }
@@ -385,12 +398,12 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
     // fetch sits on the issue path; lanes 0..15 issue the tile's query-row copies in parallel.
     if (lane == 0) {
       tma_prefetch_desc(&tmap_q);
-      tma_prefetch_desc(&tmap_po);
     }
     uint32_t q_used = 0, q_parity_bits = 0;   // lane 0: per query buffer, issued at least once / parity of the last issue
     // A group's query rows are gathered again by every block they selected: keep them in L2.
     const uint64_t pol_q = l2_policy_evict_last();
     int4 ra = make_int4(-1, 0, 0, 0), rb = make_int4(0, 0, 0, 0), rc = rb, rd = rb;   // record of tile (batch + lane)
+    int cur = -1, nbucket = -1;
     for (int i = 0; i < ntile; ++i) {
       if (__any_sync(0xFFFFFFFFu, s_abort != 0)) break;
       if ((i & 31) == 0 && i + lane < ntile) {
@@ -417,6 +430,18 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
         }
       }
       if (!__shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0)) break;
+      // S(i-3) is done, so P(i-5) was written and tile i-7's rows are stored: its record may go
+      const int bucket = __shfl_sync(0xFFFFFFFFu, ra.x, src);
+      if (bucket != cur) { ++nbucket; cur = bucket; }
+      if (lane == src) {
+        int4* rec = s_rec[i % ATP8_RECS];
+        rec[0] = make_int4(nbucket, ra.y, ra.z, ra.w);
+        rec[1] = rb;
+        rec[2] = rc;
+        rec[3] = rd;
+        mbar_arrive(&rec_full[i % ATP8_RECS]);
+      }
+      __syncwarp();
       // query rows of the tile's entries (MMA row 16e + head), [half][128 rows][64 dims] swizzled:
       // lane 2e + half issues entry e's half
       {
@@ -616,41 +641,28 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
     const int r = quarter * 32 + lane;            // MMA row = entry * 16 + head
     const int e = r >> 4, h = r & 15;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const float LN2 = 0.69314718055994531f;
     const uint64_t pol_stream = l2_policy_evict_first();
-    uint8_t* stage = o_s + w * ATTP_STAGE;
+    uint8_t* stage = o_s + w * ATTP_STAGE + e * 4096 + h * 16;
     const int nj = (ntile - w + 1) / 2;
-    // the fields this row needs of its tiles, prefetched one tile ahead
-    struct RowRec { int g, b, off, n, ent, bucket; float ks, vs; };
-    auto load_row = [&](int tile) -> RowRec {
-      const int4* p = a.tile_rec + static_cast<long>(tile) * 4;
-      const int4 h0 = __ldg(p);
-      const int4 h1 = __ldg(p + 1);
-      RowRec rr;
-      rr.bucket = h0.x; rr.g = h0.z; rr.b = h0.w; rr.off = h1.x; rr.n = h1.y & 15;
-      rr.ks = __int_as_float(h1.z); rr.vs = __int_as_float(h1.w);
-      rr.ent = __ldg(reinterpret_cast<const int*>(p + 2) + e);
-      return rr;
+    int4 h0 = make_int4(0, 0, 0, 0), h1 = h0;      // the record of tile j, and this row's entry
+    int ent = 0;
+    auto next_record = [&](int i) -> bool {
+      if (!mbar_wait_warp(&rec_full[i % ATP8_RECS], static_cast<uint32_t>((i / ATP8_RECS) & 1), &s_abort)) return false;
+      const int4* rec = s_rec[i % ATP8_RECS];
+      h0 = rec[0];
+      h1 = rec[1];
+      ent = reinterpret_cast<const int*>(rec + 2)[e];
+      return true;
     };
-    RowRec nxt{};
-    int other = -1;                                // bucket of the tile between this group's last one and the next
-    if (nj > 0) nxt = load_row(tile_of(w));
-    if (w == 1 && nj > 0) other = __ldg(&a.tile_rec[static_cast<long>(tile_of(0)) * 4].x);
-    int last_bucket = -1, nbuckets = 0;            // of this CTA's tiles so far
-    for (int j = 0; j < nj; ++j) {               // exit decisions are uniform over the warp
-      const int i = 2 * j + w;
-      const RowRec rec = nxt;
-      if (other != -1 && other != last_bucket) { ++nbuckets; last_bucket = other; }
-      if (rec.bucket != last_bucket) { ++nbuckets; last_bucket = rec.bucket; }
-      if (j + 1 < nj) {
-        nxt = load_row(tile_of(i + 2));
-        other = __ldg(&a.tile_rec[static_cast<long>(tile_of(i + 1)) * 4].x);
-      }
-      const float sc = fmaxf(a.scale_log2 * fabsf(rec.ks), 1e-36f);   // not 0: the masked -inf * 0 is NaN
-      const bool valid = e < rec.n;
-      const int ent = rec.ent;
-      const int t = ent >> 6, slot = ent & 63;
-      const int vis = valid ? min(128, t + rec.off - rec.b * 128 + 1) : 128;  // visible keys of the block
+    bool ok = nj == 0 || next_record(w);
+    for (int j = 0; j < nj && ok; ++j) {         // exit decisions are uniform over the warp
+      const int nbucket = h0.x, n = h1.y & 15;
+      const float ks = __int_as_float(h1.z), vs = __int_as_float(h1.w);
+      const float sc = fmaxf(a.scale_log2 * fabsf(ks), 1e-36f);   // not 0: the masked -inf * 0 is NaN
+      const bool valid = e < n;
+      const int t = ent >> 6;
+      const long part = (static_cast<long>(t) * a.Hkv + h0.z) * a.topk + (ent & 63);
+      const int vis = valid ? min(128, t + h1.x - h0.w * 128 + 1) : 128;  // visible keys of the block
 
       // ---- S = Q K^T is in TMEM: the row's 128 scores in registers, max over the visible keys
       if (!mbar_wait_warp(&s_full[w], static_cast<uint32_t>(j & 1), &s_abort)) break;
@@ -662,7 +674,7 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
       tmem_ld32(s_addr + 64, v2);
       tmem_ld32(s_addr + 96, v3);
       tmem_ld_wait();
-      if (rec.ks < 0.f) {                         // a negative scale: the scores' order is that of -S
+      if (ks < 0.f) {                         // a negative scale: the scores' order is that of -S
 #pragma unroll
         for (int c = 0; c < 32; ++c) { v0[c] = -v0[c]; v1[c] = -v1[c]; v2[c] = -v2[c]; v3[c] = -v3[c]; }
       }
@@ -706,9 +718,13 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[w]);
+      // ---- while the tensor cores multiply: the row's statistics, the next record
+      if (lane == 0) bulk_wait_read_all();        // lanes 0 and 16: their previous stores have left the staging rows
+      if (lane == 16) bulk_wait_read_all();
       const float l = l0 + l1;
+      if (j + 1 < nj) ok = next_record(2 * j + 2 + w);
 
-      // ---- O = P V is in TMEM: read it, release the accumulator, then O / l as bf16 to this warp's rows
+      // ---- O = P V is in TMEM: read it, release the accumulator, O as bf16 to this warp's rows
       if (!mbar_wait_warp(&o_full[w], static_cast<uint32_t>(j & 1), &s_abort)) break;
       tc_fence_after();
       float o0[32], o1[32], o2[32], o3[32];
@@ -721,48 +737,24 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_empty[w]);
-      if (lane == 0) bulk_wait_read_all();        // this warp's previous stores have left its staging rows
-      __syncwarp();
-      // a NaN among the V rows that this row sees (the converters took it out)
-      const int4 vn = *reinterpret_cast<const int4*>(s_vnan[(nbuckets - 1) & 3]);
-      const float inv = min(min(vn.x, vn.y), min(vn.z, vn.w)) < vis ? __uint_as_float(0x7FC00000u) : rec.vs / l;
-      const unsigned long long inv2 = pair(inv, inv);
-      float y0, y1;
 #pragma unroll
-      for (int q8 = 0; q8 < 16; ++q8) {
-        const int col = q8 * 8;                   // output dims col .. col+7
-        const float* ov = q8 < 4 ? o0 + col : q8 < 8 ? o1 + col - 32 : q8 < 12 ? o2 + col - 64 : o3 + col - 96;
-        uint4 wv;
-        unpair(mul2(pair(ov[0], ov[1]), inv2), y0, y1);
-        wv.x = pack_bf16(y0, y1);
-        unpair(mul2(pair(ov[2], ov[3]), inv2), y0, y1);
-        wv.y = pack_bf16(y0, y1);
-        unpair(mul2(pair(ov[4], ov[5]), inv2), y0, y1);
-        wv.z = pack_bf16(y0, y1);
-        unpair(mul2(pair(ov[6], ov[7]), inv2), y0, y1);
-        wv.w = pack_bf16(y0, y1);
-        *reinterpret_cast<uint4*>(stage + (col >> 6) * 16384 + sw128_offset(r, (col & 63) * 2)) = wv;
+      for (int c = 0; c < 16; ++c) {              // output dims 8c .. 8c+7
+        const float* ov = c < 4 ? o0 + c * 8 : c < 8 ? o1 + c * 8 - 32 : c < 12 ? o2 + c * 8 - 64 : o3 + c * 8 - 96;
+        *reinterpret_cast<uint4*>(stage + c * 256) = make_uint4(pack_bf16(ov[0], ov[1]), pack_bf16(ov[2], ov[3]),
+                                                                pack_bf16(ov[4], ov[5]), pack_bf16(ov[6], ov[7]));
       }
-      if (valid)
-        a.part_lse[(static_cast<long>(t) * a.Hq + rec.g * ATTP_G + h) * a.topk + slot] = (mc + log2f(l)) * LN2;
       fence_proxy_async_smem();
-      const int ent_hi = __shfl_sync(0xFFFFFFFFu, ent, 16);   // entry 2*quarter + 1 (lanes 16..31)
       __syncwarp();
-      if (lane == 0) {
-#pragma unroll
-        for (int k2 = 0; k2 < 2; ++k2) {
-          const int ee = 2 * quarter + k2;
-          if (ee < rec.n) {
-            const int en = k2 ? ent_hi : ent;
-            const int y = ((en >> 6) * a.topk + (en & 63)) * a.Hq + rec.g * ATTP_G;
-            tma_store_2d_hint(&tmap_po, stage + ee * 2048, 0, y, pol_stream);
-            tma_store_2d_hint(&tmap_po, stage + 16384 + ee * 2048, 64, y, pol_stream);
-          }
-        }
+      if ((lane & 15) == 0) {                     // the entry's first head stores its rows
+        if (valid) bulk_store_hint(a.part_o + part * 2048, stage, 4096, pol_stream);
         bulk_commit();
       }
+      // a NaN among the V rows that this row sees (the converters took it out)
+      const int4 vn = *reinterpret_cast<const int4*>(s_vnan[nbucket & 3]);
+      const float inv = min(min(vn.x, vn.y), min(vn.z, vn.w)) < vis ? __uint_as_float(0x7FC00000u) : vs / l;
+      if (valid) a.part_lse[part * ATTP_G + h] = make_float2(mc + log2f(l), inv);
     }
-    if (lane == 0) bulk_wait_all();               // partial stores complete before exit
+    bulk_wait_all();                              // partial stores complete before exit
   }
   __syncwarp();
   tc_fence_before();
@@ -773,8 +765,8 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
 
 // ------------------------------------------------------------------ merge
 struct MergeFp8Args {
-  const __nv_bfloat16* part_o;   // [total_q][topk][Hq][128]
-  const float* part_lse;         // [total_q][Hq][topk]
+  const __nv_bfloat16* part_o;   // [total_q][Hkv][topk][2048], as the tiles' kernel leaves them
+  const float2* part_lse;        // [total_q][Hkv][topk][16 heads]
   const int32_t* block_idx;      // [total_q][Hkv][topk]
   const int32_t* q_start;
   __nv_bfloat16* out;            // [total_q][Hq][128]
@@ -782,53 +774,48 @@ struct MergeFp8Args {
   int num_seqs, Hq, Hkv, topk;
 };
 
-// attn_merge_kernel (one CTA per (row, group): 16 heads x 16 threads x 8 output dims, every load of eight slots issued
-// before the first is used) that leaves rows behind the last sequence as they were, slots that were left out
-// (lse = -inf) unread, and lets a NaN through.
+// out = sum_b w_b O_b, w_b = 2^(lse_b - max) (v_scale / l)_b / sum 2^(lse - max), over the partials of a row and group.
+// One CTA per (row, group): 16 heads x 16 threads x 8 output dims, every load of eight slots issued before the first is
+// used.  Rows behind the last sequence are left as they were, slots without a partial (not selected, or lse = -inf)
+// count nothing, a NaN gets through.
 __global__ void __launch_bounds__(256) attn_merge_fp8_kernel(const MergeFp8Args a) {
-  __shared__ float s_w[ATTP_G][MRG_MAXK];   // per head and slot: exp(lse - max), or -1 (no partial)
+  __shared__ float s_l[MRG_MAXK][ATTP_G], s_f[MRG_MAXK][ATTP_G];
   const int t = blockIdx.x / a.Hkv, g = blockIdx.x % a.Hkv;
   if (t >= __ldg(a.q_start + a.num_seqs)) return;
-  const int h = threadIdx.x >> 4, d8 = threadIdx.x & 15;
+  const int h = threadIdx.x & 15, d8 = threadIdx.x >> 4;
   const int head = g * ATTP_G + h;
-  const int32_t* sel = a.block_idx + (static_cast<long>(t) * a.Hkv + g) * a.topk;
-  const float* pl = a.part_lse + (static_cast<long>(t) * a.Hq + head) * a.topk;
-  float mx = -1e30f;                        // finite: a row of NaN partials stays NaN
-  for (int s = d8; s < a.topk; s += 16)
-    if (__ldg(sel + s) >= 0) mx = fmaxf(mx, __ldg(pl + s));
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));   // the head's 16 lanes
+  const long first = static_cast<long>(blockIdx.x) * a.topk;            // of the row and group's slots
+  const uint4* po = reinterpret_cast<const uint4*>(a.part_o) + first * 256 + threadIdx.x;
   for (int s = d8; s < a.topk; s += 16) {
-    float w = -1.f;
-    if (__ldg(sel + s) >= 0) {
-      const float l = __ldg(pl + s);
-      if (l != -INFINITY) w = __expf(l - mx);
-    }
-    s_w[h][s] = w;
+    float2 v = make_float2(-INFINITY, 0.f);
+    if (__ldg(a.block_idx + first + s) >= 0) v = __ldg(a.part_lse + first * ATTP_G + s * ATTP_G + h);
+    s_l[s][h] = v.x;
+    s_f[s][h] = v.y;
   }
-  __syncwarp();                             // a head's 16 threads share one warp
-  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  __syncthreads();
+  float mx = -1e30f;                        // finite: a row of NaN partials stays NaN
+  for (int s = 0; s < a.topk; ++s) mx = fmaxf(mx, s_l[s][h]);
   float wsum = 0.f;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   // 8 slots per round, every partial load of the round issued before the first is used
-  const __nv_bfloat16* po = a.part_o + (static_cast<long>(t) * a.topk * a.Hq + head) * 128 + d8 * 8;
   for (int s0 = 0; s0 < a.topk; s0 += 8) {
     uint4 o[8];
     float w[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const int s = s0 + k;
-      w[k] = s < a.topk ? s_w[h][s] : -1.f;
-      o[k] = w[k] != -1.f ? __ldcs(reinterpret_cast<const uint4*>(po + static_cast<long>(s) * a.Hq * 128))
-                          : make_uint4(0u, 0u, 0u, 0u);
+      w[k] = s < a.topk ? s_l[s][h] : -INFINITY;
+      o[k] = w[k] != -INFINITY ? __ldcs(po + static_cast<long>(s) * 256) : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      if (w[k] == -1.f) continue;
-      wsum += w[k];
-      acc[0] = fmaf(w[k], bf16lo(o[k].x), acc[0]); acc[1] = fmaf(w[k], bf16hi(o[k].x), acc[1]);
-      acc[2] = fmaf(w[k], bf16lo(o[k].y), acc[2]); acc[3] = fmaf(w[k], bf16hi(o[k].y), acc[3]);
-      acc[4] = fmaf(w[k], bf16lo(o[k].z), acc[4]); acc[5] = fmaf(w[k], bf16hi(o[k].z), acc[5]);
-      acc[6] = fmaf(w[k], bf16lo(o[k].w), acc[6]); acc[7] = fmaf(w[k], bf16hi(o[k].w), acc[7]);
+      if (w[k] == -INFINITY) continue;
+      const float e = exp2f(w[k] - mx), f = e * s_f[s0 + k][h];
+      wsum += e;
+      acc[0] = fmaf(f, bf16lo(o[k].x), acc[0]); acc[1] = fmaf(f, bf16hi(o[k].x), acc[1]);
+      acc[2] = fmaf(f, bf16lo(o[k].y), acc[2]); acc[3] = fmaf(f, bf16hi(o[k].y), acc[3]);
+      acc[4] = fmaf(f, bf16lo(o[k].z), acc[4]); acc[5] = fmaf(f, bf16hi(o[k].z), acc[5]);
+      acc[6] = fmaf(f, bf16lo(o[k].w), acc[6]); acc[7] = fmaf(f, bf16hi(o[k].w), acc[7]);
     }
   }
   const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
@@ -838,7 +825,8 @@ __global__ void __launch_bounds__(256) attn_merge_fp8_kernel(const MergeFp8Args 
   r.z = pack_bf16(acc[4] * inv, acc[5] * inv);
   r.w = pack_bf16(acc[6] * inv, acc[7] * inv);
   *reinterpret_cast<uint4*>(a.out + (static_cast<long>(t) * a.Hq + head) * 128 + d8 * 8) = r;
-  if (a.lse && d8 == 0) a.lse[static_cast<long>(t) * a.Hq + head] = wsum == 0.f ? -INFINITY : mx + __logf(wsum);
+  if (a.lse && d8 == 0)
+    a.lse[static_cast<long>(t) * a.Hq + head] = wsum == 0.f ? -INFINITY : (mx + log2f(wsum)) * 0.69314718055994531f;
 }
 
 }  // namespace msa

@@ -845,7 +845,7 @@ PrefillFp8Ws prefill_fp8_plan(const msa_config_t* c, const msa_batch_t* b) {
   w.starts = take(kMaxCtas * 4);
   w.bases = take(w.nbuckets * 8);
   w.tile_rec = take(static_cast<size_t>(w.max_tiles) * 64);
-  w.part_lse = take(static_cast<size_t>(b->total_q) * c->num_q_heads * c->topk * 4);
+  w.part_lse = take(static_cast<size_t>(b->total_q) * c->num_q_heads * c->topk * 8);
   w.part_o = take(static_cast<size_t>(b->total_q) * c->topk * c->num_q_heads * c->head_dim * 2);
   w.bytes = o;
   return w;
@@ -966,7 +966,7 @@ msa_status_t msa_attn_prefill_fp8(const msa_config_t* cfg, const msa_batch_t* ba
   s.bases = reinterpret_cast<unsigned long long*>(ws + w.bases);
   s.entries = reinterpret_cast<int2*>(ws + w.part_o);
   s.tile_rec = reinterpret_cast<int4*>(ws + w.tile_rec);
-  s.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
+  s.part_lse = reinterpret_cast<float2*>(ws + w.part_lse);
   s.num_seqs = batch->num_seqs;
   s.total_q = batch->total_q;
   s.Hq = Hq;
@@ -987,14 +987,12 @@ msa_status_t msa_attn_prefill_fp8(const msa_config_t* cfg, const msa_batch_t* ba
   if ((st = launched()) != MSA_OK) return st;
   CUDA_TRY(launch_overlapped(msa::sched_fp8_bases_kernel, static_cast<unsigned>((w.nbuckets + 1023) / 1024), 256, 0, stream, s));
   CUDA_TRY(launch_overlapped(msa::sched_fp8_place_kernel, static_cast<unsigned>((w.entries + 255) / 256), 256, 0, stream, s));
-  CUtensorMap tq, tpo;
+  CUtensorMap tq;
   {
     const uint64_t dims[2] = {128, static_cast<uint64_t>(batch->total_q) * Hq};
-    const uint64_t dims_po[2] = {128, static_cast<uint64_t>(batch->total_q) * k * Hq};
     const uint64_t strides[1] = {256};
     const uint32_t box[2] = {64, 16};
     if ((st = make_map(&tq, q, 2, dims, strides, box)) != MSA_OK) return st;
-    if ((st = make_map(&tpo, ws + w.part_o, 2, dims_po, strides, box)) != MSA_OK) return st;
   }
   msa::AttnPrefillFp8Args a{};
   a.tile_rec = s.tile_rec;
@@ -1002,12 +1000,14 @@ msa_status_t msa_attn_prefill_fp8(const msa_config_t* cfg, const msa_batch_t* ba
   a.starts = s.starts;
   a.k_cache = static_cast<const uint8_t*>(k_cache_e4m3);
   a.v_cache = static_cast<const uint8_t*>(v_cache_e4m3);
+  a.part_o = reinterpret_cast<__nv_bfloat16*>(ws + w.part_o);
   a.part_lse = s.part_lse;
   a.Hq = Hq;
+  a.Hkv = Hkv;
   a.topk = k;
   a.scale_log2 = softmax_scale(cfg) * 1.4426950408889634f;
   CUDA_TRY(set_smem(msa::attn_prefill_fp8_kernel, msa::ATTP_SMEM));
-  CUDA_TRY(launch_overlapped(msa::attn_prefill_fp8_kernel, sms, msa::ATP8_THREADS, msa::ATTP_SMEM, stream, tq, tpo, a));
+  CUDA_TRY(launch_overlapped(msa::attn_prefill_fp8_kernel, sms, msa::ATP8_THREADS, msa::ATTP_SMEM, stream, tq, a));
   msa::MergeFp8Args m{};
   m.part_o = reinterpret_cast<const __nv_bfloat16*>(ws + w.part_o);
   m.part_lse = s.part_lse;
