@@ -339,7 +339,7 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
   // has been read (one arrival per warp).  k_full, v_full: a bucket's tile is widened (one arrival per converter
   // warp); k_empty, v_empty: its last S, its last P V is done.
   __shared__ uint64_t k_full, k_empty, v_full, v_empty, q_full[ATTP_QBUF], q_empty[ATTP_QBUF], s_full[2], p_full[2], o_full[2],
-      o_empty[2], rec_full[ATP8_RECS], drain_bar;
+      o_empty[2], rec_full[ATP8_RECS], drain_bar[2];
   __shared__ int4 s_rec[ATP8_RECS][4];            // the softmax warps' records (the first field: which bucket of this CTA's)
   __shared__ __align__(16) int s_vnan[4][4];      // per bucket (a ring) and converter warp: its first V row with a NaN code, or 128
   __shared__ uint32_t s_tmem;
@@ -363,7 +363,7 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
       mbar_init(&o_empty[i], 4);
     }
     for (int i = 0; i < ATP8_RECS; ++i) mbar_init(&rec_full[i], 1);
-    mbar_init(&drain_bar, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&drain_bar[i], 1);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -459,61 +459,30 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
     }
   } else if (warp == 1) {
    if (lane == 0) {
-    // ------------------------------------------------------------ UMMA issuer
-    // Tile i: S(i) = Q K^T into S[i % 2] (A and B from shared memory), then O[(i-1) % 2] = P(i-1) V with
-    // P(i-1) read from TMEM over the first half of S[(i-1) % 2].  S(i) overwrites the columns P V(i-2)
-    // read: this thread issued P V(i-2) first, and its MMAs run in issue order.
-    // This one thread's instruction latency is on the critical path: descriptors are built once
-    // (only the 14-bit start address, in 16-byte units, moves) and ring positions are counters.
+    // ------------------------------------------------------------ S issuer
+    // Tile i: S(i) = Q K^T into S[i % 2] (A and B from shared memory).  S(i) overwrites the columns that P V(i-2) reads.
+    // One thread's instruction latency is on the critical path: descriptors are built once (only the 14-bit start
+    // address, in 16-byte units, moves) and ring positions are counters.
     const uint32_t id_s = idesc_bf16(128, 128, false, false);
-    const uint32_t id_pv = idesc_f16(128, 128, true);
     const uint64_t qdesc0 = sdesc_sw128(smem_u32(q_s), 16, 1024);
     const uint64_t kdesc0 = sdesc_sw128(smem_u32(k_s), 16, 1024);
-    const uint64_t vdesc0 = sdesc_sw128(smem_u32(v_s), 16384, 1024);
     int qb = 0;
     uint32_t qph = 0;
     int cur_bucket = -1;
     uint32_t kvit = 0;
-    bool pv_pending = false;
-    bool v_wait = true;
-    uint32_t vit = 0;
-    auto issue_pv = [&](int j, bool last) -> bool {  // O[j%2] = P[j%2] V; last: the last of its bucket
-      if (v_wait && !mbar_wait(&v_full, vit & 1, &s_abort)) return false;
-      v_wait = false;
-      const int pb = j & 1;
-      const uint32_t ph = static_cast<uint32_t>((j >> 1) & 1);
-      if (!mbar_wait(&p_full[pb], ph, &s_abort)) return false;
-      if (!mbar_wait(&o_empty[pb], ph ^ 1u, &s_abort)) return false;   // tile j-2's O has been read
-      tc_fence_after();
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk)   // 16 keys per step: 2048 bytes of V rows
-        umma_bf16_ts(tmem + ATTP_TM_O + pb * 128, tmem + ATTP_TM_S + pb * 128 + kk * 8, vdesc0 + 128 * kk, id_pv,
-                     kk > 0 ? 1u : 0u);
-      umma_commit(&o_full[pb]);
-      if (last) {
-        umma_commit(&v_empty);
-        ++vit;
-        v_wait = true;
-      }
-      return true;
-    };
-    bool ok = true;
     int nbucket = ntile > 0 ? __ldg(&a.tile_rec[static_cast<long>(tile_of(0)) * 4].x) : -1;
-    for (int i = 0; i < ntile && ok && !s_abort; ++i) {
+    for (int i = 0; i < ntile && !s_abort; ++i) {
       const int bucket = nbucket;
       if (i + 1 < ntile) nbucket = __ldg(&a.tile_rec[static_cast<long>(tile_of(i + 1)) * 4].x);
-      const bool change = bucket != cur_bucket;
-      if (change) {
-        // the previous bucket's last S is issued: K may be replaced, and its last P V does not wait for that
-        if (cur_bucket >= 0) umma_commit(&k_empty);
-        if (pv_pending && !issue_pv(i - 1, true)) break;
-        pv_pending = false;
+      if (bucket != cur_bucket) {
+        if (cur_bucket >= 0) umma_commit(&k_empty);      // the previous bucket's last S is issued: K may be replaced
         if (!mbar_wait(&k_full, kvit & 1, &s_abort)) break;
         ++kvit;
         cur_bucket = bucket;
       }
       const int sb = i & 1;
       if (!mbar_wait(&q_full[qb], qph, &s_abort)) break;
+      if (i >= 2 && !mbar_wait(&o_full[sb], static_cast<uint32_t>((i >> 1) - 1) & 1u, &s_abort)) break;   // P V(i-2)
       tc_fence_after();
       const uint32_t d = tmem + ATTP_TM_S + sb * 128;
       const uint64_t qd = qdesc0 + static_cast<uint64_t>((qb * ATTP_QBYTES) >> 4);
@@ -525,13 +494,45 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
       umma_commit(&s_full[sb]);
       umma_commit(&q_empty[qb]);
       if (++qb == ATTP_QBUF) { qb = 0; qph ^= 1u; }
-      if (pv_pending) ok = issue_pv(i - 1, false);
-      pv_pending = true;
     }
-    if (ok && !s_abort && pv_pending) issue_pv(ntile - 1, true);
     if (s_abort) {
-      umma_commit(&drain_bar);
-      mbar_wait_drain(&drain_bar, 0);
+      umma_commit(&drain_bar[0]);
+      mbar_wait_drain(&drain_bar[0], 0);
+    }
+   }
+  } else if (warp == 2) {
+   if (lane == 0) {
+    // ------------------------------------------------------------ P V issuer
+    // O[i % 2] = P(i) V, P(i) read from TMEM over the first half of S[i % 2].
+    const uint32_t id_pv = idesc_f16(128, 128, true);
+    const uint64_t vdesc0 = sdesc_sw128(smem_u32(v_s), 16384, 1024);
+    uint32_t vit = 0;
+    bool v_wait = true;
+    int bucket = ntile > 0 ? __ldg(&a.tile_rec[static_cast<long>(tile_of(0)) * 4].x) : -1;
+    for (int i = 0; i < ntile && !s_abort; ++i) {
+      const int next = i + 1 < ntile ? __ldg(&a.tile_rec[static_cast<long>(tile_of(i + 1)) * 4].x) : -1;
+      const int pb = i & 1;
+      const uint32_t ph = static_cast<uint32_t>((i >> 1) & 1);
+      if (v_wait && !mbar_wait(&v_full, vit & 1, &s_abort)) break;
+      v_wait = false;
+      if (!mbar_wait(&o_empty[pb], ph ^ 1u, &s_abort)) break;   // tile i-2's O has been read
+      if (!mbar_wait(&p_full[pb], ph, &s_abort)) break;
+      tc_fence_after();
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)   // 16 keys per step: 2048 bytes of V rows
+        umma_bf16_ts(tmem + ATTP_TM_O + pb * 128, tmem + ATTP_TM_S + pb * 128 + kk * 8, vdesc0 + 128 * kk, id_pv,
+                     kk > 0 ? 1u : 0u);
+      umma_commit(&o_full[pb]);
+      if (next != bucket) {              // the last of its bucket
+        umma_commit(&v_empty);
+        ++vit;
+        v_wait = true;
+        bucket = next;
+      }
+    }
+    if (s_abort) {
+      umma_commit(&drain_bar[1]);
+      mbar_wait_drain(&drain_bar[1], 0);
     }
    }
   }
