@@ -57,6 +57,10 @@ class _CBatch(ctypes.Structure):
 
 
 _lib_handle = None
+# _bind.so, once the library is loaded: these calls' checks and the call itself, natively.  A function of it answers None
+# for arguments that do not fit; the Python code behind each use then says what is wrong with them.
+_calls = None
+_BOUND = ("msa_attn_decode_fp8", "msa_attn_prefill_fp8", "msa_qknorm_rope_insert_fp8", "msa_advance_batch")
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -105,7 +109,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         getattr(lib, name).restype = ctypes.c_size_t
     lib.msa_status_string.restype = ctypes.c_char_p
     lib.msa_last_error.restype = ctypes.c_char_p
-    _lib_handle = lib
+    global _calls
+    try:
+        from . import _bind
+    except ImportError as e:
+        raise RuntimeError("_bind.so is missing or does not fit this torch: build it with "
+                           "`python -m block_sparse_long_13_b200.build --force`") from e
+    _bind.setup(*(ctypes.cast(getattr(lib, name), P).value for name in _BOUND))
+    _calls, _lib_handle = _bind, lib
     return lib
 
 
@@ -333,30 +344,34 @@ def decode_fp8_workspace_bytes(cfg: Config, batch: Batch) -> int:
                                                              ctypes.byref(batch._c(host_only=True))))
 
 
-def _attn_fp8(fn, cfg, batch, q, k_cache, v_cache, k_scale, v_scale, block_idx, out, lse, workspace, stream):
-    rows = (batch.total_q, cfg.num_q_heads)
-    bf16, heads = torch.bfloat16, rows + (cfg.head_dim,)
-    nbytes = workspace.numel() if workspace is not None else 0
-    ptrs = _pointers((q, bf16, heads, "q"), *_fp8_cache(cfg, batch, k_cache, v_cache, k_scale, v_scale),
-                     (block_idx, torch.int32, (batch.total_q, cfg.num_kv_heads, cfg.topk), "block_idx"),
-                     (out, bf16, heads, "out"), (lse, torch.float32, rows, "lse"),
-                     (workspace, torch.uint8, (nbytes,), "workspace"), *_batch_arrays(batch))
-    _check(fn(cfg._c(), batch._c(host_only=True), *ptrs[:9], nbytes, _stream_here(stream)))
+def _attn_fp8(prefill, cfg, batch, q, k_cache, v_cache, k_scale, v_scale, block_idx, out, lse, workspace, stream):
+    lib = _lib_handle or load_library()
+    status = _calls.attn(prefill, cfg, batch, q, k_cache, v_cache, k_scale, v_scale, block_idx, out, lse, workspace, stream)
+    if status is None:
+        rows = (batch.total_q, cfg.num_q_heads)
+        bf16, heads = torch.bfloat16, rows + (cfg.head_dim,)
+        nbytes = workspace.numel() if workspace is not None else 0
+        ptrs = _pointers((q, bf16, heads, "q"), *_fp8_cache(cfg, batch, k_cache, v_cache, k_scale, v_scale),
+                         (block_idx, torch.int32, (batch.total_q, cfg.num_kv_heads, cfg.topk), "block_idx"),
+                         (out, bf16, heads, "out"), (lse, torch.float32, rows, "lse"),
+                         (workspace, torch.uint8, (nbytes,), "workspace"), *_batch_arrays(batch))
+        fn = lib.msa_attn_prefill_fp8 if prefill else lib.msa_attn_decode_fp8
+        status = fn(cfg._c(), batch._c(host_only=True), *ptrs[:9], nbytes, _stream_here(stream))
+    if status:
+        _check(status)
 
 
 def attn_decode_fp8(cfg: Config, batch: Batch, q, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale, block_idx, out, lse=None,
                     workspace=None, stream=None) -> None:
     """attn_decode over a cache of e4m3 codes (uint8 [num_pages][num_kv_heads][128][128]) with a scale for each
     (page, KV head) (fp32 [num_pages][num_kv_heads]); value = code * scale.  For few queries per sequence."""
-    _attn_fp8(load_library().msa_attn_decode_fp8, cfg, batch, q, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale, block_idx,
-              out, lse, workspace, stream)
+    _attn_fp8(False, cfg, batch, q, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale, block_idx, out, lse, workspace, stream)
 
 
 def attn_prefill_fp8(cfg: Config, batch: Batch, q, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale, block_idx, out, lse=None,
                      workspace=None, stream=None) -> None:
     """attn_decode_fp8's results, organised for many queries per sequence."""
-    _attn_fp8(load_library().msa_attn_prefill_fp8, cfg, batch, q, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale, block_idx,
-              out, lse, workspace, stream)
+    _attn_fp8(True, cfg, batch, q, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale, block_idx, out, lse, workspace, stream)
 
 
 def qknorm_rope_insert_fp8(cfg: Config, batch: Batch, q, k_new, v_new, q_norm_w, k_norm_w, q_out, k_cache_e4m3,
@@ -364,12 +379,20 @@ def qknorm_rope_insert_fp8(cfg: Config, batch: Batch, q, k_new, v_new, q_norm_w,
                            eps: float = 1e-6, stream=None) -> None:
     """qknorm_rope_insert into an 8-bit cache (see include/msa.h): the queries go to q_out (q itself or another
     buffer), the new rows become codes, and the scales of their pages follow."""
-    bf16, heads, new = torch.bfloat16, (batch.total_q, cfg.num_q_heads, cfg.head_dim), (batch.total_q, cfg.num_kv_heads, cfg.head_dim)
-    ptrs = _pointers((q, bf16, heads, "q"), (k_new, bf16, new, "k_new"), (v_new, bf16, new, "v_new"),
-                     (q_norm_w, bf16, new[2:], "q_norm_w"), (k_norm_w, bf16, new[2:], "k_norm_w"), (q_out, bf16, heads, "q_out"),
-                     *_fp8_cache(cfg, batch, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale), *_batch_arrays(batch))
-    _check(load_library().msa_qknorm_rope_insert_fp8(cfg._c(), batch._c(host_only=True), *ptrs[:10], int(rotary_dim),
-                                                     float(rope_theta), float(eps), _stream_here(stream)))
+    lib = _lib_handle or load_library()
+    status = _calls.insert(cfg, batch, q, k_new, v_new, q_norm_w, k_norm_w, q_out, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale,
+                          rotary_dim, rope_theta, eps, stream)
+    if status is None:
+        bf16, heads = torch.bfloat16, (batch.total_q, cfg.num_q_heads, cfg.head_dim)
+        new = (batch.total_q, cfg.num_kv_heads, cfg.head_dim)
+        ptrs = _pointers((q, bf16, heads, "q"), (k_new, bf16, new, "k_new"), (v_new, bf16, new, "v_new"),
+                         (q_norm_w, bf16, new[2:], "q_norm_w"), (k_norm_w, bf16, new[2:], "k_norm_w"),
+                         (q_out, bf16, heads, "q_out"),
+                         *_fp8_cache(cfg, batch, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale), *_batch_arrays(batch))
+        status = lib.msa_qknorm_rope_insert_fp8(cfg._c(), batch._c(host_only=True), *ptrs[:10], int(rotary_dim),
+                                                float(rope_theta), float(eps), _stream_here(stream))
+    if status:
+        _check(status)
 
 
 def advance_batch(delta, ctx_len, page_table, free_ring, pool, ctx_len_out, pool_out, q_start, slot_map=None,
@@ -378,18 +401,24 @@ def advance_batch(delta, ctx_len, page_table, free_ring, pool, ctx_len_out, pool
     given back to the ring, and ctx_len_out, q_start and page_table then serve as a Batch.  ctx_len_out may be ctx_len
     and pool_out may be pool.  All tensors int32; nothing is read back to the host: pool_out[2] says on the device how
     many pages the step lacked (0: done, -1: arguments that do not fit)."""
-    if page_table.dim() != 2:
-        raise MsaError(MSA_ERR_INVALID_ARG, "page_table must be [num_seqs][max_blocks_per_seq]")
-    n, width = page_table.shape
-    pages, rows = free_ring.numel(), slot_map.numel() if slot_map is not None else 0
-    i32 = torch.int32
-    ptrs = _pointers((delta, i32, (n,), "delta"), (ctx_len, i32, (n,), "ctx_len"), (page_table, i32, (n, width), "page_table"),
-                     (free_ring, i32, (pages,), "free_ring"), (pool, i32, (4,), "pool"), (ctx_len_out, i32, (n,), "ctx_len_out"),
-                     (pool_out, i32, (4,), "pool_out"), (q_start, i32, (n + 1,), "q_start"),
-                     (slot_map, i32, (rows,), "slot_map"))
-    if rows == 0:
-        ptrs[8] = 0                    # an empty slot map is none
-    _check(load_library().msa_advance_batch(n, width, pages, int(block_size), *ptrs, rows, _stream_here(stream)))
+    lib = _lib_handle or load_library()
+    status = _calls.advance(delta, ctx_len, page_table, free_ring, pool, ctx_len_out, pool_out, q_start, slot_map, block_size,
+                           stream)
+    if status is None:
+        if page_table.dim() != 2:
+            raise MsaError(MSA_ERR_INVALID_ARG, "page_table must be [num_seqs][max_blocks_per_seq]")
+        n, width = page_table.shape
+        pages, rows = free_ring.numel(), slot_map.numel() if slot_map is not None else 0
+        i32 = torch.int32
+        ptrs = _pointers((delta, i32, (n,), "delta"), (ctx_len, i32, (n,), "ctx_len"),
+                         (page_table, i32, (n, width), "page_table"), (free_ring, i32, (pages,), "free_ring"),
+                         (pool, i32, (4,), "pool"), (ctx_len_out, i32, (n,), "ctx_len_out"), (pool_out, i32, (4,), "pool_out"),
+                         (q_start, i32, (n + 1,), "q_start"), (slot_map, i32, (rows,), "slot_map"))
+        if rows == 0:
+            ptrs[8] = 0                    # an empty slot map is none
+        status = lib.msa_advance_batch(n, width, pages, int(block_size), *ptrs, rows, _stream_here(stream))
+    if status:
+        _check(status)
 
 
 def merge_partials(outs, lses, out, lse=None, stream=None) -> None:

@@ -1,4 +1,5 @@
-"""Build libmsa.so (the MSA C-ABI library) in-tree for sm_100a with nvcc.
+"""Build libmsa.so (the MSA C-ABI library) in-tree for sm_100a with nvcc, and _bind.so (the Python calls that are made
+for every token, natively) with g++.
 
     python -m block_sparse_long_13_b200.build [--force]
 """
@@ -8,10 +9,12 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmsa.so")
+BIND = os.path.join(HERE, "_bind.so")
 ROOT = os.path.dirname(HERE)
 HEADER = os.path.join(ROOT, "include", "msa.h")
 
@@ -36,22 +39,43 @@ def sources():
     return [os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith((".cu", ".cuh"))] + [HEADER]
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+def bind_sources():
+    return [os.path.join(CSRC, "bind.cpp"), HEADER]
+
+
+def up_to_date(lib: str = LIB, made_of=None) -> bool:
+    if not os.path.exists(lib):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(s) <= t for s in sources())
+    t = os.path.getmtime(lib)
+    return all(os.path.getmtime(s) <= t for s in (sources() if made_of is None else made_of))
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB
-    tmp = LIB + ".tmp"
-    cmd = [nvcc_path(), *NVCC_FLAGS, "-o", tmp, os.path.join(CSRC, "msa.cu")]
+def _run(cmd, lib: str, verbose: bool) -> None:
+    tmp = lib + ".tmp"
+    cmd = [*cmd, "-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
-    os.replace(tmp, LIB)
+    os.replace(tmp, lib)
+
+
+def build_bind(verbose: bool = False) -> None:
+    import torch
+    at = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    includes = [sysconfig.get_paths()["include"], os.path.join(at, "include"),
+                os.path.join(at, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
+    _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *[x for i in includes for x in ("-isystem", i)],
+          os.path.join(CSRC, "bind.cpp"), "-L" + os.path.join(at, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch",
+          "-ltorch_python"], BIND, verbose)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    if force or not up_to_date():
+        _run([nvcc_path(), *NVCC_FLAGS, os.path.join(CSRC, "msa.cu")], LIB, verbose)
+    if force or not up_to_date(BIND, bind_sources()):
+        build_bind(verbose)
     return LIB
 
 

@@ -1,6 +1,7 @@
 """The 8-bit K/V cache without a GPU: the calls' checks of their arguments, and
 the oracle of its arithmetic against hand-worked values."""
 import ctypes
+import sys
 
 import numpy as np
 import pytest
@@ -146,6 +147,37 @@ def test_binding_refuses_wrong_shapes_and_cpu_tensors(lib):
     for name, t in dict(delta=i32(3), ctx=i32(1), table=i32(8), pool=i32(2), ctx2=i32(4), pool2=i32(3), qs=i32(2)).items():
         _refused(msa.advance_batch, *{**adv, name: t}.values())
     assert "CUDA tensor" in _refused(msa.advance_batch, *adv.values())
+
+
+def test_native_calls_leave_what_does_not_fit_to_python(lib):
+    """None for whatever is not exactly right, no Python error left behind and no reference lost or kept."""
+    cfg, b = msa.Config(), _batch(4)
+    z = lambda *s, dtype=torch.bfloat16: torch.zeros(*s, dtype=dtype)  # noqa: E731
+    args = [z(4, 64, 128), z(2, 4, 128, 128, dtype=torch.uint8), z(2, 4, 128, 128, dtype=torch.uint8),
+            z(2, 4, dtype=torch.float32), z(2, 4, dtype=torch.float32), z(4, 4, 16, dtype=torch.int32), z(4, 64, 128), None,
+            None, None]
+    held = [cfg, b, b.q_start, b.ctx_len, b.page_table, *args[:7], cfg.num_q_heads]
+    before = [sys.getrefcount(x) for x in held[:-1]]
+    ints = [torch.zeros(n, dtype=torch.int32) for n in (2, 2, 8, 4, 2, 4, 3)]
+    for _ in range(50):
+        assert msa._calls.attn(False, cfg, b, *args) is None
+        assert msa._calls.attn(True, cfg, b, *args) is None
+        assert msa._calls.attn(False, None, b, *args) is None
+        assert msa._calls.attn(False, cfg, "batch", *args) is None
+        assert msa._calls.attn(False, cfg, b) is None
+        for i in range(len(args)):
+            assert msa._calls.attn(False, cfg, b, *args[:i], object(), *args[i + 1:]) is None
+        assert msa._calls.attn(False, msa.Config(num_q_heads=1 << 40), b, *args) is None
+        assert msa._calls.attn(False, msa.Config(softmax_scale="1"), b, *args) is None
+        assert msa._calls.insert(cfg, b, *args[:4], args[3], args[3], args[0], *args[1:5], 64, 1e4, 1e-6, None) is None
+        assert msa._calls.advance(*ints[:2], torch.zeros(2, 4, dtype=torch.int32), *ints[2:], None, 128, None) is None
+        assert msa._calls.advance(*ints[:2], ints[2], *ints[2:], None, 128, None) is None
+        assert msa._calls.advance() is None
+    assert [sys.getrefcount(x) for x in held[:-1]] == before
+    with pytest.raises(TypeError):
+        msa._calls.setup(1, 2)
+    with pytest.raises((TypeError, ValueError)):
+        msa._calls.setup(0, 0, 0, 0)
 
 
 def test_binding_refuses_another_device(lib, monkeypatch):

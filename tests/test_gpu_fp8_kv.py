@@ -299,6 +299,35 @@ def test_same_bits_again_on_other_pages_and_another_stream(cuda_ok, which):
         assert torch.equal(a[0], x[0]) and torch.equal(a[1], x[1])
 
 
+def test_forms_of_the_arguments(cuda_ok):
+    """Streams as objects and numbers, weights as parameters and numbers of other types give the same bits; what is of
+    the wrong type, layout or shape is refused by name."""
+    c = Case(31, ctx=[300, 129], nq=[2, 1])
+    d = c.device()
+    ref, _ = c.run()
+    ws = torch.zeros(c.size(c.cfg, c.batch), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    scale = float(c.cfg.head_dim) ** -0.5
+    for cfg, q, stream in ((c.cfg, d[0], side), (c.cfg, d[0], side.cuda_stream), (c.cfg, d[0], 0),
+                           (c.cfg, torch.nn.Parameter(d[0]), None),
+                           (msa.Config(64, 4, idx_heads=4, topk=np.int64(16), softmax_scale=np.float64(scale)), d[0], None),
+                           (msa.Config(64, 4, idx_heads=4, topk=16, softmax_scale=0), d[0], None)):
+        out = torch.full_like(d[0], 7.0)
+        side.wait_stream(torch.cuda.current_stream())
+        c.fn(cfg, c.batch, q, *d[1:], out, None, ws, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref)
+    good = [*d, torch.empty_like(d[0]), None, ws]
+    for i, bad, what in ((0, d[0].float(), "q must be torch.bfloat16"), (0, d[0].transpose(0, 1).contiguous().transpose(0, 1), "contiguous"),
+                         (1, d[1].view(torch.int8), "k_cache_e4m3 must be"), (3, d[3].double(), "k_scale must be"),
+                         (5, d[5].long(), "block_idx must be"), (6, good[6][:-1], "out has shape"), (7, ref, "lse has shape"),
+                         (8, ws.view(1, -1), "workspace has shape"), (8, ws.cpu(), "CUDA tensor")):
+        with pytest.raises(msa.MsaError) as e:
+            c.fn(c.cfg, c.batch, *good[:i], bad, *good[i + 1:])
+        assert e.value.status == msa.MSA_ERR_INVALID_ARG and what in str(e.value)
+
+
 @pytest.mark.parametrize("which", FORMS)
 def test_graphs_with_their_own_workspaces(cuda_ok, which):
     """Two captured calls, replayed in turn and with new inputs in place, give what the eager calls give."""
