@@ -18,8 +18,9 @@
 // the call's rows (CTA = window of 128 rows, which holds one such block for each sequence that crosses a
 // block border in it): num_seqs + total_q / 128 CTAs a head, no search by the host.
 // At most 148 CTAs walk the pieces, so that all of them run from the start and q_norm_rope_kernel, which needs nothing
-// from them, may be launched beside them (an ordinary launch after them: 166 us for 16,384 rows, 83 and 86 for the two).
-// q_norm_rope_kernel: one CTA a row, in and out by bulk copies; bound by HBM (6.2 TB/s).
+// from them, may be launched beside them (16,384 rows: 166 us behind one another, 106 beside).
+// q_norm_rope_kernel: one CTA a row, in and out by bulk copies; bound by HBM.  Both together
+// move 5.5 TB/s at 16,384 rows; a single step of 64 rows takes 8.9 us, which two launches and four dependent look-ups set.
 //
 // Angles: theta^(-2i/r) / 2 pi turns a position, as 64-bit fractions of a turn from a table that the host fills.  Their
 // product with the position modulo 2^64 is the fraction of a turn, off by 2^-64 a position (2^-40 at 2^24), in two
@@ -32,10 +33,12 @@
 
 namespace msa {
 
-constexpr int KVI_THREADS = 512;                       // 32 half-warps, a row's head each
-constexpr int KVI_ROWS = KVI_THREADS / 16;             // rows at a time
-constexpr int KVI_ITERS = 128 / KVI_ROWS;              // rows of a full page per half-warp
-constexpr int KVI_GRID = 148;                          // CTAs at most
+// Threads of a CTA, a row's head to 16 of them, each with ITERS rows in registers.  Sequences of at most 8 rows (a step's
+// tokens) take CTAs of 128 threads with one row each: the code is a quarter, four CTAs leave room on an SM, and 64 rows
+// take 8.9 us instead of 10.0.  Other calls want a page's 128 rows in one CTA.
+constexpr int KVI_THREADS = 512, KVI_ITERS = 4, KVI_GRID = 148;         // of CTAs at most KVI_GRID
+constexpr int KVI_FEW_THREADS = 128, KVI_FEW_ROWS = 8, KVI_FEW_GRID = 4 * 148;
+static_assert(KVI_THREADS / 16 * KVI_ITERS == 128 && KVI_FEW_THREADS / 16 == KVI_FEW_ROWS, "rows of a CTA");
 
 struct RopeTable { unsigned long long turns[QKR_D / 2]; };   // theta^(-2i/r) / (2 pi) modulo 1, times 2^64, i < rotary_dim / 2
 
@@ -50,7 +53,7 @@ struct KvInsertArgs {
   const int32_t* q_start;
   const int32_t* ctx_len;
   const int32_t* page_table;
-  int num_seqs, total_q, Hkv, max_blocks, num_pages, rotary_dim, pieces;
+  int num_seqs, total_q, Hkv, max_blocks, num_pages, rotary_dim, pieces, max_q;
   float eps;
 };
 
@@ -66,8 +69,9 @@ __device__ __forceinline__ float finite_abs(float x) {   // |x|, 0 for infinitie
 }
 
 // Codes of the older rows of a page after its scale grew: e4m3(code * ratio).
+template <int THREADS>
 __device__ __forceinline__ void rescale_codes(uint8_t* tile, int rows, float ratio) {
-  for (int i = threadIdx.x; i < rows * 8; i += KVI_THREADS) {
+  for (int i = threadIdx.x; i < rows * 8; i += THREADS) {
     uint4* p = reinterpret_cast<uint4*>(tile) + i;
     uint4 w = *p;
     uint32_t* u = reinterpret_cast<uint32_t*>(&w);
@@ -81,9 +85,18 @@ __device__ __forceinline__ void rescale_codes(uint8_t* tile, int rows, float rat
   }
 }
 
+// e4m3(y / s) of eight numbers, for scales that are no power of two: out of line, so that its divisions do not stand eight
+// times in the code that every call runs through.
+__device__ __noinline__ uint2 divided_codes(float4 x, float4 y, float s) {
+  return make_uint2(e4m3x4_of(__fdiv_rn(x.x, s), __fdiv_rn(x.y, s), __fdiv_rn(x.z, s), __fdiv_rn(x.w, s)),
+                    e4m3x4_of(__fdiv_rn(y.x, s), __fdiv_rn(y.y, s), __fdiv_rn(y.z, s), __fdiv_rn(y.w, s)));
+}
+
 // One piece: rows t0 .. t0 + n - 1 at positions p0 .. of one block, KV head g, page `page` (valid).
+template <int THREADS, int ITERS>
 __device__ __forceinline__ void kv_insert_piece(const KvInsertArgs& a, const RopeTable& tab, int t0, int p0, int n, int page,
-                                                int g, float (&s_max)[2][KVI_THREADS / 32]) {
+                                                int g, float (&s_max)[2][THREADS / 32]) {
+  constexpr int ROWS = THREADS / 16;                     // at a time
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hl = lane & 15;
   const int row0 = warp * 2 + (lane >> 4);
   const int slot0 = p0 & 127;
@@ -96,11 +109,11 @@ __device__ __forceinline__ void kv_insert_piece(const KvInsertArgs& a, const Rop
   const int qa = rot ? hl : 2 * P + 2 * (hl - P);
   const int ca = 4 * qa, cb = 4 * (rot ? hl + P : qa + 1);
 
-  uint2 ka[KVI_ITERS], kb[KVI_ITERS];
-  uint4 vv[KVI_ITERS];
+  uint2 ka[ITERS], kb[ITERS];
+  uint4 vv[ITERS];
 #pragma unroll
-  for (int it = 0; it < KVI_ITERS; ++it) {
-    const int r = it * KVI_ROWS + row0;
+  for (int it = 0; it < ITERS; ++it) {
+    const int r = it * ROWS + row0;
     ka[it] = kb[it] = make_uint2(0u, 0u);
     vv[it] = make_uint4(0u, 0u, 0u, 0u);
     if (r < n) {
@@ -117,11 +130,11 @@ __device__ __forceinline__ void kv_insert_piece(const KvInsertArgs& a, const Rop
 #pragma unroll
   for (int u = 0; u < 4; ++u) turns[u] = rot ? tab.turns[ca + u] : 0ull;
 
-  float ky[KVI_ITERS][8];
+  float ky[ITERS][8];
   float kmax = 0.f, vmax = 0.f;
 #pragma unroll
-  for (int it = 0; it < KVI_ITERS; ++it) {
-    if (it * KVI_ROWS >= n) break;                             // uniform
+  for (int it = 0; it < ITERS; ++it) {
+    if (it * ROWS >= n) break;                             // uniform
     float xa[4] = {bf16lo(ka[it].x), bf16hi(ka[it].x), bf16lo(ka[it].y), bf16hi(ka[it].y)};
     float xb[4] = {bf16lo(kb[it].x), bf16hi(kb[it].x), bf16lo(kb[it].y), bf16hi(kb[it].y)};
     float ss = 0.f;
@@ -130,7 +143,7 @@ __device__ __forceinline__ void kv_insert_piece(const KvInsertArgs& a, const Rop
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
     const float inv = rsqrtf(ss * (1.f / QKR_D) + a.eps);
-    const int p = p0 + it * KVI_ROWS + row0;
+    const int p = p0 + it * ROWS + row0;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const float ya = xa[u] * inv * wa[u], yb = xb[u] * inv * wb[u];
@@ -139,7 +152,7 @@ __device__ __forceinline__ void kv_insert_piece(const KvInsertArgs& a, const Rop
       ky[it][u] = rot ? ya * cs - yb * sn : ya;
       ky[it][4 + u] = rot ? yb * cs + ya * sn : yb;
     }
-    if (it * KVI_ROWS + row0 < n) {                            // rows past the piece hold nothing
+    if (it * ROWS + row0 < n) {                            // rows past the piece hold nothing
 #pragma unroll
       for (int u = 0; u < 8; ++u) kmax = fmaxf(kmax, finite_abs(ky[it][u]));
       const uint32_t* w = reinterpret_cast<const uint32_t*>(&vv[it]);
@@ -155,7 +168,7 @@ __device__ __forceinline__ void kv_insert_piece(const KvInsertArgs& a, const Rop
   if (lane == 0) { s_max[0][warp] = kmax; s_max[1][warp] = vmax; }
   __syncthreads();                                       // every thread has read the old scales
 #pragma unroll
-  for (int w = 0; w < KVI_THREADS / 32; ++w) {
+  for (int w = 0; w < THREADS / 32; ++w) {
     kmax = fmaxf(kmax, s_max[0][w]);
     vmax = fmaxf(vmax, s_max[1][w]);
   }
@@ -171,35 +184,40 @@ __device__ __forceinline__ void kv_insert_piece(const KvInsertArgs& a, const Rop
   uint8_t* kt = a.k_cache + tile * (128 * QKR_D);
   uint8_t* vt = a.v_cache + tile * (128 * QKR_D);
 #pragma unroll
-  for (int it = 0; it < KVI_ITERS; ++it) {
-    const int r = it * KVI_ROWS + row0;
+  for (int it = 0; it < ITERS; ++it) {
+    const int r = it * ROWS + row0;
     if (r >= n) break;
     uint8_t* kr = kt + (slot0 + r) * QKR_D;
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&vv[it]);
     float z[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) z[u] = exact ? ky[it][u] * ki : __fdiv_rn(ky[it][u], ks);
-    *reinterpret_cast<uint32_t*>(kr + ca) = e4m3x4_of(z[0], z[1], z[2], z[3]);
-    *reinterpret_cast<uint32_t*>(kr + cb) = e4m3x4_of(z[4], z[5], z[6], z[7]);
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(&vv[it]);
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      z[2 * u] = exact ? bf16lo(w[u]) * vi : __fdiv_rn(bf16lo(w[u]), vs);
-      z[2 * u + 1] = exact ? bf16hi(w[u]) * vi : __fdiv_rn(bf16hi(w[u]), vs);
+    for (int u = 0; u < 4; ++u) { z[2 * u] = bf16lo(w[u]); z[2 * u + 1] = bf16hi(w[u]); }
+    uint2 kc, vc;
+    if (exact) {
+      const float* y = ky[it];
+      kc = make_uint2(e4m3x4_of(y[0] * ki, y[1] * ki, y[2] * ki, y[3] * ki), e4m3x4_of(y[4] * ki, y[5] * ki, y[6] * ki, y[7] * ki));
+      vc = make_uint2(e4m3x4_of(z[0] * vi, z[1] * vi, z[2] * vi, z[3] * vi), e4m3x4_of(z[4] * vi, z[5] * vi, z[6] * vi, z[7] * vi));
+    } else {
+      const float* y = ky[it];
+      kc = divided_codes(make_float4(y[0], y[1], y[2], y[3]), make_float4(y[4], y[5], y[6], y[7]), ks);
+      vc = divided_codes(make_float4(z[0], z[1], z[2], z[3]), make_float4(z[4], z[5], z[6], z[7]), vs);
     }
-    *reinterpret_cast<uint2*>(vt + (slot0 + r) * QKR_D + 8 * hl) =
-        make_uint2(e4m3x4_of(z[0], z[1], z[2], z[3]), e4m3x4_of(z[4], z[5], z[6], z[7]));
+    *reinterpret_cast<uint32_t*>(kr + ca) = kc.x;
+    *reinterpret_cast<uint32_t*>(kr + cb) = kc.y;
+    *reinterpret_cast<uint2*>(vt + (slot0 + r) * QKR_D + 8 * hl) = vc;
   }
-  if (slot0 > 0 && k_grown) rescale_codes(kt, slot0, k_held ? __fdiv_rn(k_old, ks) : 0.f);
-  if (slot0 > 0 && v_grown) rescale_codes(vt, slot0, v_held ? __fdiv_rn(v_old, vs) : 0.f);
+  if (slot0 > 0 && k_grown) rescale_codes<THREADS>(kt, slot0, k_held ? __fdiv_rn(k_old, ks) : 0.f);
+  if (slot0 > 0 && v_grown) rescale_codes<THREADS>(vt, slot0, v_held ? __fdiv_rn(v_old, vs) : 0.f);
   if (tid == 0) {
     if (k_grown) a.k_scale[tile] = ks;
     if (v_grown) a.v_scale[tile] = vs;
   }
 }
 
-__global__ void __launch_bounds__(KVI_THREADS, 1)
+template <int THREADS, int ITERS>
+__global__ void __launch_bounds__(THREADS, ITERS == 1 ? 4 : 1)
 kv_insert_fp8_kernel(const KvInsertArgs a, const __grid_constant__ RopeTable tab) {
-  __shared__ float s_max[2][KVI_THREADS / 32];
+  __shared__ float s_max[2][THREADS / 32];
   __shared__ int s_t[128], s_p[128], s_s[128], s_cnt[4];
   pdl_launch_dependents();                               // the queries' kernel needs nothing from this one
   // the cache page of sequence s's block b; -1 (and flagged) if there is none
@@ -216,12 +234,12 @@ kv_insert_fp8_kernel(const KvInsertArgs a, const __grid_constant__ RopeTable tab
     if (i < a.num_seqs) {                                // the block that the sequence's first new row falls in
       const int t0 = __ldg(a.q_start + i), nq = __ldg(a.q_start + i + 1) - t0, p0 = __ldg(a.ctx_len + i) - nq;
       if (nq <= 0) continue;
-      if (p0 < 0 || t0 < 0 || t0 + nq > a.total_q) {
+      if (p0 < 0 || t0 < 0 || t0 + nq > a.total_q || nq > a.max_q) {
         if (tid == 0) flag_error(MSA_DEV_BOUNDS);
         continue;
       }
       const int page = page_of(i, p0 >> 7);
-      if (page >= 0) kv_insert_piece(a, tab, t0, p0, min(nq, 128 - (p0 & 127)), page, g, s_max);
+      if (page >= 0) kv_insert_piece<THREADS, ITERS>(a, tab, t0, p0, min(nq, 128 - (p0 & 127)), page, g, s_max);
       __syncthreads();                                   // s_max is written again
       continue;
     }
@@ -235,7 +253,8 @@ kv_insert_fp8_kernel(const KvInsertArgs a, const __grid_constant__ RopeTable tab
         s = find_seq(a.q_start, a.num_seqs, t);
         const int end = __ldg(a.q_start + s + 1);
         p = __ldg(a.ctx_len + s) - end + t;
-        lead = t != __ldg(a.q_start + s) && p > 0 && (p & 127) == 0;
+        const int first = __ldg(a.q_start + s);
+        lead = t != first && end - first <= a.max_q && p > 0 && (p & 127) == 0;
       }
       vote = __ballot_sync(0xFFFFFFFFu, lead);
       if (lane == 0) s_cnt[warp] = __popc(vote);
@@ -251,7 +270,7 @@ kv_insert_fp8_kernel(const KvInsertArgs a, const __grid_constant__ RopeTable tab
     for (int j = 0; j < n_lead; ++j) {
       const int page = page_of(s_s[j], s_p[j] >> 7);
       if (page >= 0)
-        kv_insert_piece(a, tab, s_t[j], s_p[j], min(128, min(rows, __ldg(a.q_start + s_s[j] + 1)) - s_t[j]), page, g, s_max);
+        kv_insert_piece<THREADS, ITERS>(a, tab, s_t[j], s_p[j], min(128, min(rows, __ldg(a.q_start + s_s[j] + 1)) - s_t[j]), page, g, s_max);
       __syncthreads();                                   // s_max is written again
     }
     __syncthreads();                                     // and so are the window's lists
@@ -268,7 +287,11 @@ struct QNormRopeArgs {
   float eps;
 };
 
-__global__ void __launch_bounds__(QKR_THREADS)
+// CTAS of an SM at least: 8 take 32 registers a thread, which 16,384 rows run faster with (106 us instead of 111) and 64 rows
+// slower (10.3 instead of 8.9).
+constexpr int QNR_MANY = 6 * 148;                      // rows: more than are in flight without the limit
+template <int CTAS>
+__global__ void __launch_bounds__(QKR_THREADS, CTAS)
 q_norm_rope_kernel(const QNormRopeArgs a, const __grid_constant__ RopeTable tab) {
   extern __shared__ __align__(128) uint8_t qnr_dsmem[];
   __nv_bfloat16* xs = reinterpret_cast<__nv_bfloat16*>(qnr_dsmem);   // [Hq][128]
@@ -333,7 +356,7 @@ q_norm_rope_kernel(const QNormRopeArgs a, const __grid_constant__ RopeTable tab)
   if (tid == 0) {
     bulk_store(a.q_out + static_cast<long>(t) * a.Hq * QKR_D, xs, bytes);
     bulk_commit();
-    bulk_wait_all();
+    bulk_wait_read_all();                              // shared memory stays valid until the copy has read it
   }
 }
 

@@ -1069,7 +1069,13 @@ msa_status_t msa_qknorm_rope_insert_fp8(const msa_config_t* cfg, const msa_batch
   a.eps = eps;
   const unsigned pieces = static_cast<unsigned>(batch->num_seqs) + (static_cast<unsigned>(batch->total_q) + 127u) / 128u;
   a.pieces = static_cast<int>(pieces) * a.Hkv;
-  msa::kv_insert_fp8_kernel<<<std::min(a.pieces, msa::KVI_GRID), msa::KVI_THREADS, 0, stream>>>(a, tab);
+  a.max_q = batch->max_q_per_seq;
+  if (batch->max_q_per_seq <= msa::KVI_FEW_ROWS)
+    msa::kv_insert_fp8_kernel<msa::KVI_FEW_THREADS, 1>
+        <<<std::min(a.pieces, msa::KVI_FEW_GRID), msa::KVI_FEW_THREADS, 0, stream>>>(a, tab);
+  else
+    msa::kv_insert_fp8_kernel<msa::KVI_THREADS, msa::KVI_ITERS>
+        <<<std::min(a.pieces, msa::KVI_GRID), msa::KVI_THREADS, 0, stream>>>(a, tab);
   if ((st = launched()) != MSA_OK) return st;
   msa::QNormRopeArgs qa{};
   qa.q = static_cast<const __nv_bfloat16*>(q);
@@ -1082,11 +1088,10 @@ msa_status_t msa_qknorm_rope_insert_fp8(const msa_config_t* cfg, const msa_batch
   qa.Hq = cfg->num_q_heads;
   qa.rotary_dim = rotary_dim;
   qa.eps = eps;
-  CUDA_TRY(set_smem(msa::q_norm_rope_kernel, smem));
-  CUDA_TRY(cudaFuncSetAttribute(msa::q_norm_rope_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                cudaSharedmemCarveoutMaxShared));
-  CUDA_TRY(launch_overlapped(msa::q_norm_rope_kernel, static_cast<unsigned>(batch->total_q), msa::QKR_THREADS, smem, stream,
-                             qa, tab));
+  const auto q_kernel = batch->total_q > msa::QNR_MANY ? msa::q_norm_rope_kernel<8> : msa::q_norm_rope_kernel<1>;
+  CUDA_TRY(set_smem(q_kernel, smem));
+  CUDA_TRY(cudaFuncSetAttribute(q_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared));
+  CUDA_TRY(launch_overlapped(q_kernel, static_cast<unsigned>(batch->total_q), msa::QKR_THREADS, smem, stream, qa, tab));
   return MSA_OK;
 }
 

@@ -409,8 +409,10 @@ def _check_insert(c, got):
         for which in (1, 2):
             a, b = value[kind == which], np.clip(target[kind == which], -448, 448)
             assert (np.abs(a - b) <= (2.0 ** -4 + 1e-5) * np.abs(b) + 2.0 ** -10 + 1e-5).all(), (which, float(np.abs(a - b).max()))
-        # older codes that stay normal lose nothing when a power of two grows to another
-        normal = (kind == 1)[..., None] & (np.abs(target) >= 2.0 ** -6)
+        # older codes that stay normal lose nothing when a power of two grows to another (code * old / new is then the code
+        # with another exponent; from any other old scale the product has more bits and is rounded, which the bound allows)
+        power = np.frexp(old)[0] == 0.5
+        normal = (kind == 1)[..., None] & (np.abs(target) >= 2.0 ** -6) & power[:, :, None, None]
         assert np.array_equal(value[normal], target[normal])
 
 
@@ -433,6 +435,32 @@ def test_insert_matches_oracle(cuda_ok, shape, in_place):
     if c["pad"]:
         tail = c["q"][:1].expand(c["pad"], -1, -1) if in_place else torch.full((c["pad"], *c["q"].shape[1:]), 7.0, dtype=torch.bfloat16)
         assert torch.equal(got[0][c["T"]:].cpu(), tail)
+
+
+@pytest.mark.parametrize("shape", [dict(ctx=[8, 135, 500, 132], nq=[8, 8, 8, 8]), dict(ctx=[9, 135, 500, 132], nq=[9, 8, 3, 8]),
+                                   dict(ctx=[*range(1, 701)], nq=[1] * 700, kv=1), dict(ctx=[1300, 40], nq=[1100, 3], kv=1)],
+                         ids=["8 rows", "9 rows", "more pieces than CTAs", "rows of several waves"])
+def test_insert_at_the_borders_of_its_forms(cuda_ok, shape):
+    """Old scales are any numbers here: those that stay divide the new rows."""
+    c = _insert_case(23, **shape)
+    rng = np.random.default_rng(24)
+    for x in c["scales"]:
+        x[:] = rng.uniform(0.004, 0.05, size=x.shape)
+    got = _insert(c)
+    assert msa.device_status() == msa.MSA_OK
+    _check_insert(c, got)
+
+
+def test_insert_refuses_more_rows_than_the_batch_says(cuda_ok):
+    """A sequence longer than max_q_per_seq is recorded, and the caches keep what they held for it."""
+    for most in (2, 100):
+        c = _insert_case(26, ctx=[300, 50], nq=[200, 1], kv=2)
+        c["batch"].max_q_per_seq = most
+        got = _insert(c)
+        assert msa.device_status() == msa.MSA_ERR_DEVICE_BOUNDS
+        kept = c["table"][0][c["table"][0] >= 0]
+        for x, before in zip(got[1:], (*c["codes"], *c["scales"])):
+            assert np.array_equal(x[torch.from_numpy(kept).long().cuda()].cpu().numpy(), before[kept])
 
 
 @pytest.mark.parametrize("rotary_dim,theta", [(8, 1e4), (56, 5e6), (128, 10.0), (64, 1.0)])
