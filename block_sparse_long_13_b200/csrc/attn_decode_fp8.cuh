@@ -35,6 +35,9 @@
 // softmax is longer than the 0.74 us that its 32 KiB take at the copy bandwidth: hence two groups.  An MMA as
 // narrow as these takes 47 clocks whatever its N (measured, N <= 64), so the high and low parts are the two halves of
 // one N = 32 operand, and the halves of the result are added when it is read.  Every wait is bounded.
+// Measured: 64 rows over 128K keys, 16 blocks, 4 groups: 28.3 us with the merge (134 MB of codes: 4.8 TB/s), of which 20 us
+// are the stream (0.65 us a block and CTA) and 8 set-up, first look-ups, first pass through the code and merge; one row over
+// 32K 10.2 us; 32 x 4 verify rows 49.4 us.  Before the roles shared one barrier a slot the 64 rows took 45.7 us.
 #pragma once
 #include "attn_decode.cuh"
 #include "e4m3.cuh"

@@ -11,6 +11,14 @@
 // Feeding the tensor cores with the codes, as the decode form does, would take P in two 8-bit parts, 256 more
 // instructions for each row of 128 keys in the softmax warps that set this kernel's pace; a block's widening is 20 to 45
 // instructions per 16 codes, once for all tokens that selected it, in warps of their own.
+//
+// Bound by the chain of a tile's steps: two softmax groups take tiles in turn, a pair of tiles 6,000 clocks (scores out of
+// TMEM 430, exponentials 1,530, P V 1,100 to 1,800, output 1,400, waits), of which the tensor cores are held for 3,400 and
+// DRAM for a third.  What shortened it: records through shared memory instead of global loads whose use the registers'
+// allocation moved behind the loop (2.65 -> 2.58 ms), partials without the division and the part's statistics behind the
+// stores (2.42), S and P V issued by two threads (mixed chunks 239 -> 230 us).  Partials stored straight from registers
+// were slower (2.58 instead of 2.42 ms), P handed over in halves changed nothing.  The last 16,384 rows of 128K take 2.4 ms:
+// schedule 0.04, tiles 1.58 (700 TFLOP/s of S and P V), merge 0.68 at 6.4 TB/s.
 #pragma once
 #include "attn_prefill.cuh"
 #include "e4m3.cuh"
