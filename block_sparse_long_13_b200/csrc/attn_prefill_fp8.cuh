@@ -784,10 +784,11 @@ struct MergeFp8Args {
 };
 
 // out = sum_b w_b O_b, w_b = 2^(lse_b - max) (v_scale / l)_b / sum 2^(lse - max), over the partials of a row and group.
-// One CTA per (row, group): 16 heads x 16 threads x 8 output dims, every load of eight slots issued before the first is
-// used.  Rows behind the last sequence are left as they were, slots without a partial (not selected, or lse = -inf)
-// count nothing, a NaN gets through.
-__global__ void __launch_bounds__(256) attn_merge_fp8_kernel(const MergeFp8Args a) {
+// One CTA per (row, group): 16 heads x 16 threads x 8 output dims, every load of four slots issued before the first is
+// used, six CTAs an SM (eight slots and four CTAs: 2,048 rows of one group 45.8 us instead of 44.6, the rest alike).  Rows
+// behind the last sequence are left as they were, slots without a partial (not selected, or lse = -inf) count nothing, a
+// NaN gets through.
+__global__ void __launch_bounds__(256, 6) attn_merge_fp8_kernel(const MergeFp8Args a) {
   __shared__ float s_l[MRG_MAXK][ATTP_G], s_f[MRG_MAXK][ATTP_G];
   const int t = blockIdx.x / a.Hkv, g = blockIdx.x % a.Hkv;
   if (t >= __ldg(a.q_start + a.num_seqs)) return;
@@ -806,18 +807,18 @@ __global__ void __launch_bounds__(256) attn_merge_fp8_kernel(const MergeFp8Args 
   for (int s = 0; s < a.topk; ++s) mx = fmaxf(mx, s_l[s][h]);
   float wsum = 0.f;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  // 8 slots per round, every partial load of the round issued before the first is used
-  for (int s0 = 0; s0 < a.topk; s0 += 8) {
-    uint4 o[8];
-    float w[8];
+  // 4 slots per round, every partial load of the round issued before the first is used
+  for (int s0 = 0; s0 < a.topk; s0 += 4) {
+    uint4 o[4];
+    float w[4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < 4; ++k) {
       const int s = s0 + k;
       w[k] = s < a.topk ? s_l[s][h] : -INFINITY;
       o[k] = w[k] != -INFINITY ? __ldcs(po + static_cast<long>(s) * 256) : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < 4; ++k) {
       if (w[k] == -INFINITY) continue;
       const float e = exp2f(w[k] - mx), f = e * s_f[s0 + k][h];
       wsum += e;
