@@ -16,9 +16,10 @@
 // TMEM 430, exponentials 1,530, P V 1,100 to 1,800, output 1,400, waits), of which the tensor cores are held for 3,400 and
 // DRAM for a third.  What shortened it: records through shared memory instead of global loads whose use the registers'
 // allocation moved behind the loop (2.65 -> 2.58 ms), partials without the division and the part's statistics behind the
-// stores (2.42), S and P V issued by two threads (mixed chunks 239 -> 230 us).  Partials stored straight from registers
-// were slower (2.58 instead of 2.42 ms), P handed over in halves changed nothing.  The last 16,384 rows of 128K take 2.4 ms:
-// schedule 0.04, tiles 1.58 (700 TFLOP/s of S and P V), merge 0.68 at 6.4 TB/s.
+// stores (2.42), S and P V issued by two threads (mixed chunks 239 -> 230 us), K and V in two buffers each, for which the
+// partials go straight from the registers to memory instead of by way of shared memory (230 -> 221 and 2.42 ms alike; that
+// alone, with one buffer: 235 and 2.58).  P handed over in halves changed nothing.  The last 16,384 rows of 128K take 2.4
+// ms: schedule 0.04, tiles 1.58 (700 TFLOP/s of S and P V), merge 0.68 at 6.4 TB/s.
 #pragma once
 #include "attn_prefill.cuh"
 #include "e4m3.cuh"
@@ -29,8 +30,10 @@ namespace msa {
 // Warpgroup 0: producer and issuer warps; 1: converters; 2, 3: softmax.  Register split (setmaxnreg) of the launch's
 // 128 a thread: 128 * (56 + 88 + 184 + 184) = 65536.
 constexpr int ATP8_THREADS = 512;
+constexpr int ATP8_QBUF = 3;     // gathered query tiles in flight
+constexpr int ATP8_SMEM = ATP8_QBUF * ATTP_QBYTES + 4 * ATTP_KVBYTES + 1024;
 constexpr int ATP8_RECS = 8;     // ring of records
-constexpr int ATP8_RUN = 64;      // tiles of a CTA and round
+constexpr int ATP8_RUN = 64;     // tiles of a CTA and round
 constexpr int ATP8_REGS_CTRL = 56, ATP8_REGS_CONV = 88, ATP8_REGS_SOFTMAX = 184;
 static_assert(ATP8_REGS_CTRL + ATP8_REGS_CONV + 2 * ATP8_REGS_SOFTMAX <= 4 * 128, "register split exceeds the launch");
 
@@ -311,21 +314,14 @@ __global__ void __launch_bounds__(256) sched_fp8_place_kernel(const SchedFp8Args
 }
 
 // ------------------------------------------------------------------ tiles
-// bulk_store with an L2 policy
-__device__ __forceinline__ void bulk_store_hint(void* dst, const void* src, uint32_t bytes, uint64_t policy) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group.L2::cache_hint [%0], [%1], %2, %3;"
-               ::"l"(reinterpret_cast<uint64_t>(dst)), "r"(smem_u32(src)), "r"(bytes), "l"(policy)
-               : "memory");
-}
-
 struct AttnPrefillFp8Args {
   const int4* tile_rec;      // [tiles][4] records written by sched_fp8_place_kernel
   const unsigned long long* total;   // cost << 32 | number of tiles
   const int* starts;         // [gridDim.x]
   const uint8_t* k_cache;    // [pages][Hkv][128][128] codes
   const uint8_t* v_cache;
-  // Partials of (row, group, slot): O is not divided by l and counts codes, [16 pieces of 8 dims][16 heads][8], 4 KiB that one
-  // bulk copy stores; of each head log2(sum) and v_scale / l, the factor that O still wants.
+  // Partials of (row, group, slot): O is not divided by l and counts codes, [16 pieces of 8 dims][16 heads][8], so that a
+  // warp's stores are whole lines; of each head log2(sum) and v_scale / l, the factor that O still wants.
   __nv_bfloat16* part_o;     // [total_q][Hkv][topk][2048]
   float2* part_lse;          // [total_q][Hkv][topk][16 heads]
   int Hq, Hkv, topk;
@@ -338,16 +334,17 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
   extern __shared__ __align__(1024) uint8_t dsmem[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~uintptr_t(1023));
   uint8_t* q_s = smem;                                  // 3 x 32 KiB: [half][128 rows][64]
-  uint8_t* k_s = q_s + ATTP_QBUF * ATTP_QBYTES;         // [half][128 keys][64]
-  uint8_t* v_s = k_s + ATTP_KVBYTES;                    // [half][128 keys][64]
-  uint8_t* o_s = v_s + ATTP_KVBYTES;                    // 2 x 32 KiB: [8 entries][16 pieces][16 heads][8 dims]
+  uint8_t* k_s = q_s + ATP8_QBUF * ATTP_QBYTES;         // 2 x: [half][128 keys][64]
+  uint8_t* v_s = k_s + 2 * ATTP_KVBYTES;                // 2 x: [half][128 keys][64]
 
   // Per warpgroup w (its own tile sequence, so a parity never runs two phases ahead): s_full[w] S is in
   // TMEM, p_full[w] P is in TMEM (one arrival per warp), o_full[w] O[w] holds its tile, o_empty[w] O[w]
   // has been read (one arrival per warp).  k_full, v_full: a bucket's tile is widened (one arrival per converter
-  // warp); k_empty, v_empty: its last S, its last P V is done.
-  __shared__ uint64_t k_full, k_empty, v_full, v_empty, q_full[ATTP_QBUF], q_empty[ATTP_QBUF], s_full[2], p_full[2], o_full[2],
-      o_empty[2], rec_full[ATP8_RECS], drain_bar[2];
+  // warp); k_empty, v_empty: its last S, its last P V is done.  K and V have two buffers each: a bucket's first S comes two
+  // tiles before the last P V of the bucket before it, and with one buffer every change of bucket held P V up by 2,000
+  // clocks.
+  __shared__ uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], q_full[ATP8_QBUF], q_empty[ATP8_QBUF], s_full[2],
+      p_full[2], o_full[2], o_empty[2], rec_full[ATP8_RECS], drain_bar[2];
   __shared__ int4 s_rec[ATP8_RECS][4];            // the softmax warps' records (the first field: which bucket of this CTA's)
   __shared__ __align__(16) int s_vnan[4][4];      // per bucket (a ring) and converter warp: its first V row with a NaN code, or 128
   __shared__ uint32_t s_tmem;
@@ -356,11 +353,13 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     s_abort = 0;
-    mbar_init(&k_full, 4);
-    mbar_init(&v_full, 4);
-    mbar_init(&k_empty, 1);
-    mbar_init(&v_empty, 1);
-    for (int i = 0; i < ATTP_QBUF; ++i) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&k_full[i], 4);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 4);
+      mbar_init(&v_empty[i], 1);
+    }
+    for (int i = 0; i < ATP8_QBUF; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
     }
@@ -404,9 +403,7 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
     // ------------------------------------------------------------ producer warp
     // Tile records arrive 32 at a time (one per lane, a single coalesced load), so no record
     // fetch sits on the issue path; lanes 0..15 issue the tile's query-row copies in parallel.
-    if (lane == 0) {
-      tma_prefetch_desc(&tmap_q);
-    }
+    if (lane == 0) tma_prefetch_desc(&tmap_q);
     uint32_t q_used = 0, q_parity_bits = 0;   // lane 0: per query buffer, issued at least once / parity of the last issue
     // A group's query rows are gathered again by every block they selected: keep them in L2.
     const uint64_t pol_q = l2_policy_evict_last();
@@ -427,8 +424,8 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
       const int e4 = __shfl_sync(0xFFFFFFFFu, rd.x, src), e5 = __shfl_sync(0xFFFFFFFFu, rd.y, src);
       const int e6 = __shfl_sync(0xFFFFFFFFu, rd.z, src), e7 = __shfl_sync(0xFFFFFFFFu, rd.w, src);
       bool ok = true;
-      const int qb = i % ATTP_QBUF;
-      const uint32_t qpar = static_cast<uint32_t>((i / ATTP_QBUF) & 1);
+      const int qb = i % ATP8_QBUF;
+      const uint32_t qpar = static_cast<uint32_t>((i / ATP8_QBUF) & 1);
       if (lane == 0) {
         ok = mbar_wait(&q_empty[qb], qpar ^ 1u, &s_abort);
         if (ok) {
@@ -438,7 +435,7 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
         }
       }
       if (!__shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0)) break;
-      // S(i-3) is done, so P(i-5) was written and tile i-7's rows are stored: its record may go
+      // S(i-3) is done, so P(i-5) was written and tile i-7 is over: its record may go
       const int bucket = __shfl_sync(0xFFFFFFFFu, ra.x, src);
       if (bucket != cur) { ++nbucket; cur = bucket; }
       if (lane == src) {
@@ -462,7 +459,7 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
       }
     }
     if (lane == 0 && s_abort) {                  // let issued copies land before the CTA exits
-      for (int j = 0; j < ATTP_QBUF; ++j)
+      for (int j = 0; j < ATP8_QBUF; ++j)
         if (q_used & (1u << j)) mbar_wait_drain(&q_full[j], (q_parity_bits >> j) & 1u);
     }
   } else if (warp == 1) {
@@ -474,6 +471,7 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
     const uint32_t id_s = idesc_bf16(128, 128, false, false);
     const uint64_t qdesc0 = sdesc_sw128(smem_u32(q_s), 16, 1024);
     const uint64_t kdesc0 = sdesc_sw128(smem_u32(k_s), 16, 1024);
+    uint64_t kdesc = kdesc0;
     int qb = 0;
     uint32_t qph = 0;
     int cur_bucket = -1;
@@ -483,8 +481,9 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
       const int bucket = nbucket;
       if (i + 1 < ntile) nbucket = __ldg(&a.tile_rec[static_cast<long>(tile_of(i + 1)) * 4].x);
       if (bucket != cur_bucket) {
-        if (cur_bucket >= 0) umma_commit(&k_empty);      // the previous bucket's last S is issued: K may be replaced
-        if (!mbar_wait(&k_full, kvit & 1, &s_abort)) break;
+        if (cur_bucket >= 0) umma_commit(&k_empty[(kvit & 1) ^ 1]);   // the previous bucket's last S is issued
+        if (!mbar_wait(&k_full[kvit & 1], (kvit >> 1) & 1, &s_abort)) break;
+        kdesc = kdesc0 + static_cast<uint64_t>((kvit & 1) * (ATTP_KVBYTES >> 4));
         ++kvit;
         cur_bucket = bucket;
       }
@@ -497,11 +496,11 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {   // 16 dims per step: 32 bytes within a 128-byte row, halves 16 KiB apart
         const uint32_t off16 = (kk >> 2) * 1024 + (kk & 3) * 2;
-        umma_bf16_ss(d, qd + off16, kdesc0 + off16, id_s, kk > 0 ? 1u : 0u);
+        umma_bf16_ss(d, qd + off16, kdesc + off16, id_s, kk > 0 ? 1u : 0u);
       }
       umma_commit(&s_full[sb]);
       umma_commit(&q_empty[qb]);
-      if (++qb == ATTP_QBUF) { qb = 0; qph ^= 1u; }
+      if (++qb == ATP8_QBUF) { qb = 0; qph ^= 1u; }
     }
     if (s_abort) {
       umma_commit(&drain_bar[0]);
@@ -521,18 +520,19 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
       const int next = i + 1 < ntile ? __ldg(&a.tile_rec[static_cast<long>(tile_of(i + 1)) * 4].x) : -1;
       const int pb = i & 1;
       const uint32_t ph = static_cast<uint32_t>((i >> 1) & 1);
-      if (v_wait && !mbar_wait(&v_full, vit & 1, &s_abort)) break;
+      if (v_wait && !mbar_wait(&v_full[vit & 1], (vit >> 1) & 1, &s_abort)) break;
       v_wait = false;
       if (!mbar_wait(&o_empty[pb], ph ^ 1u, &s_abort)) break;   // tile i-2's O has been read
       if (!mbar_wait(&p_full[pb], ph, &s_abort)) break;
       tc_fence_after();
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk)   // 16 keys per step: 2048 bytes of V rows
-        umma_bf16_ts(tmem + ATTP_TM_O + pb * 128, tmem + ATTP_TM_S + pb * 128 + kk * 8, vdesc0 + 128 * kk, id_pv,
+        umma_bf16_ts(tmem + ATTP_TM_O + pb * 128, tmem + ATTP_TM_S + pb * 128 + kk * 8,
+                     vdesc0 + static_cast<uint64_t>((vit & 1) * (ATTP_KVBYTES >> 4)) + 128 * kk, id_pv,
                      kk > 0 ? 1u : 0u);
       umma_commit(&o_full[pb]);
       if (next != bucket) {              // the last of its bucket
-        umma_commit(&v_empty);
+        umma_commit(&v_empty[vit & 1]);
         ++vit;
         v_wait = true;
         bucket = next;
@@ -547,9 +547,8 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
   } else if (warp < 8) {
     regs_dec<ATP8_REGS_CONV>();
     // ------------------------------------------------------------ converters: a bucket's codes to 16 bits
-    // A thread takes every 128th 16-byte piece of the tile.  K waits for the previous bucket's last S only and V for its
-    // last P V, and the next bucket's K codes are in registers by then, so a change of bucket costs the tensor
-    // cores one conversion of K.
+    // A thread takes every 128th 16-byte piece of the tile.  Its buffers are free when the last S and the last P V of
+    // the bucket before the previous one are done, so that a bucket is widened while the previous one's tiles run.
     const int ct = tid - 128;
     int4 ra = make_int4(-1, 0, 0, 0), rb = ra;               // records of tiles (batch + lane)
     int i = 0, cur = -1, row = 0, valid = 0;
@@ -594,20 +593,20 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
     }
     for (uint32_t it = 0; have && ok; ++it) {
       const bool nans = warp_has_nan(x);
-      ok = mbar_wait_warp(&k_empty, (it & 1) ^ 1, &s_abort);
+      ok = mbar_wait_warp(&k_empty[it & 1], ((it >> 1) & 1) ^ 1, &s_abort);
       if (!ok) break;
       if (nans) {                     // rare: piece by piece, out of L2 again
 #pragma unroll 1
-        for (int k = 0; k < 8; ++k) widen16_bf16<true>(k_s, k * 128 + ct, __ldg(codes(a.k_cache) + k * 128));
+        for (int k = 0; k < 8; ++k) widen16_bf16<true>(k_s + (it & 1) * ATTP_KVBYTES, k * 128 + ct, __ldg(codes(a.k_cache) + k * 128));
       } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) widen16_bf16<false>(k_s, k * 128 + ct, x[k]);
+        for (int k = 0; k < 8; ++k) widen16_bf16<false>(k_s + (it & 1) * ATTP_KVBYTES, k * 128 + ct, x[k]);
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&k_full);
+      if (lane == 0) mbar_arrive(&k_full[it & 1]);
       load(a.v_cache);
-      ok = mbar_wait_warp(&v_empty, (it & 1) ^ 1, &s_abort);
+      ok = mbar_wait_warp(&v_empty[it & 1], ((it >> 1) & 1) ^ 1, &s_abort);
       if (!ok) break;
       int bad = 128;
       if (valid < 128 || warp_has_nan(x)) {
@@ -622,17 +621,17 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
             bad = min(bad, key);
             y = without_nan(y);
           }
-          widen16_f16(v_s, k * 128 + ct, y);
+          widen16_f16(v_s + (it & 1) * ATTP_KVBYTES, k * 128 + ct, y);
         }
       } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) widen16_f16(v_s, k * 128 + ct, x[k]);
+        for (int k = 0; k < 8; ++k) widen16_f16(v_s + (it & 1) * ATTP_KVBYTES, k * 128 + ct, x[k]);
       }
       bad = __reduce_min_sync(0xFFFFFFFFu, bad);
       if (lane == 0) s_vnan[it & 3][warp - 4] = bad;
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&v_full);
+      if (lane == 0) mbar_arrive(&v_full[it & 1]);
       have = next_bucket();
       if (have) {
         load(a.k_cache);
@@ -642,7 +641,7 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
   } else {
     regs_inc<ATP8_REGS_SOFTMAX>();
     // ------------------------------------------------------------ two softmax + epilogue warpgroups
-    // Warpgroup w takes the CTA's tiles i = w, w + 2, ...; it owns S[w], P[w] and staging buffer w.
+    // Warpgroup w takes the CTA's tiles i = w, w + 2, ...; it owns S[w], P[w] and O[w].
     // Every warp runs on its own (its 32 TMEM lanes = 2 entries x 16 heads): it waits, arrives and
     // stores its rows without waiting for the other warps.
     const int w = (warp - 8) >> 2;
@@ -650,8 +649,6 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
     const int r = quarter * 32 + lane;            // MMA row = entry * 16 + head
     const int e = r >> 4, h = r & 15;
     const uint32_t lane_addr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint64_t pol_stream = l2_policy_evict_first();
-    uint8_t* stage = o_s + w * ATTP_STAGE + e * 4096 + h * 16;
     const int nj = (ntile - w + 1) / 2;
     int4 h0 = make_int4(0, 0, 0, 0), h1 = h0;      // the record of tile j, and this row's entry
     int ent = 0;
@@ -728,8 +725,6 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[w]);
       // ---- while the tensor cores multiply: the row's statistics, the next record
-      if (lane == 0) bulk_wait_read_all();        // lanes 0 and 16: their previous stores have left the staging rows
-      if (lane == 16) bulk_wait_read_all();
       const float l = l0 + l1;
       if (j + 1 < nj) ok = next_record(2 * j + 2 + w);
 
@@ -746,24 +741,20 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_empty[w]);
+      if (valid) {
+        uint4* po = reinterpret_cast<uint4*>(a.part_o + part * 2048) + h;
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {              // output dims 8c .. 8c+7
-        const float* ov = c < 4 ? o0 + c * 8 : c < 8 ? o1 + c * 8 - 32 : c < 12 ? o2 + c * 8 - 64 : o3 + c * 8 - 96;
-        *reinterpret_cast<uint4*>(stage + c * 256) = make_uint4(pack_bf16(ov[0], ov[1]), pack_bf16(ov[2], ov[3]),
-                                                                pack_bf16(ov[4], ov[5]), pack_bf16(ov[6], ov[7]));
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if ((lane & 15) == 0) {                     // the entry's first head stores its rows
-        if (valid) bulk_store_hint(a.part_o + part * 2048, stage, 4096, pol_stream);
-        bulk_commit();
+        for (int c = 0; c < 16; ++c) {            // output dims 8c .. 8c+7
+          const float* ov = c < 4 ? o0 + c * 8 : c < 8 ? o1 + c * 8 - 32 : c < 12 ? o2 + c * 8 - 64 : o3 + c * 8 - 96;
+          __stcs(po + c * 16, make_uint4(pack_bf16(ov[0], ov[1]), pack_bf16(ov[2], ov[3]), pack_bf16(ov[4], ov[5]),
+                                         pack_bf16(ov[6], ov[7])));
+        }
       }
       // a NaN among the V rows that this row sees (the converters took it out)
       const int4 vn = *reinterpret_cast<const int4*>(s_vnan[nbucket & 3]);
       const float inv = min(min(vn.x, vn.y), min(vn.z, vn.w)) < vis ? __uint_as_float(0x7FC00000u) : vs / l;
       if (valid) a.part_lse[part * ATTP_G + h] = make_float2(mc + log2f(l), inv);
     }
-    bulk_wait_all();                              // partial stores complete before exit
   }
   __syncwarp();
   tc_fence_before();

@@ -1007,8 +1007,8 @@ msa_status_t msa_attn_prefill_fp8(const msa_config_t* cfg, const msa_batch_t* ba
   a.Hkv = Hkv;
   a.topk = k;
   a.scale_log2 = softmax_scale(cfg) * 1.4426950408889634f;
-  CUDA_TRY(set_smem(msa::attn_prefill_fp8_kernel, msa::ATTP_SMEM));
-  CUDA_TRY(launch_overlapped(msa::attn_prefill_fp8_kernel, sms, msa::ATP8_THREADS, msa::ATTP_SMEM, stream, tq, a));
+  CUDA_TRY(set_smem(msa::attn_prefill_fp8_kernel, msa::ATP8_SMEM));
+  CUDA_TRY(launch_overlapped(msa::attn_prefill_fp8_kernel, sms, msa::ATP8_THREADS, msa::ATP8_SMEM, stream, tq, a));
   msa::MergeFp8Args m{};
   m.part_o = reinterpret_cast<const __nv_bfloat16*>(ws + w.part_o);
   m.part_lse = s.part_lse;
