@@ -320,9 +320,10 @@ struct AttnPrefillFp8Args {
   const int* starts;         // [gridDim.x]
   const uint8_t* k_cache;    // [pages][Hkv][128][128] codes
   const uint8_t* v_cache;
-  // Partials of (row, group, slot): O is not divided by l and counts codes, [16 pieces of 8 dims][16 heads][8], so that a
+  // Partials of (row, group, slot): O is not divided by l and counts codes, as f16 (bf16 would cost no less and take the error
+  // against 64 bits from 1.7e-3, that of the output's own rounding, to 2.3e-3), [16 pieces of 8 dims][16 heads][8], so that a
   // warp's stores are whole lines; of each head log2(sum) and v_scale / l, the factor that O still wants.
-  __nv_bfloat16* part_o;     // [total_q][Hkv][topk][2048]
+  __half* part_o;            // [total_q][Hkv][topk][2048]
   float2* part_lse;          // [total_q][Hkv][topk][16 heads]
   int Hq, Hkv, topk;
   float scale_log2;
@@ -699,7 +700,9 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
 #pragma unroll
       for (int c = 0; c < 32; ++c) mx[c & 7] = fmax3(mx[c & 7], fmaxf(v0[c], v1[c]), fmaxf(v2[c], v3[c]));
       const float m = fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], fmax3(mx[4], mx[5], mx[6]), mx[7]));
-      const float mc = (m > -INFINITY) ? m * sc : 0.f;   // -inf only on rows past the tile's entries
+      // P at most 1/2, so that a sum of 128 codes of 448 stays an f16 number with room for the rounding of m sc; -inf only on
+      // rows past the tile's entries
+      const float mc = (m > -INFINITY) ? fmaf(m, sc, 1.f) : 0.f;
       // ---- P = exp2(scale * S - max) as f16 pairs into P[w] (TMEM), two halves of 64 keys
       float l0 = 0.f, l1 = 0.f;
       const unsigned long long sc2 = pair(sc, sc), mc2 = pair(-mc, -mc);
@@ -728,7 +731,7 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
       const float l = l0 + l1;
       if (j + 1 < nj) ok = next_record(2 * j + 2 + w);
 
-      // ---- O = P V is in TMEM: read it, release the accumulator, O as bf16 to this warp's rows
+      // ---- O = P V is in TMEM: read it, release the accumulator, O as f16 to its partial
       if (!mbar_wait_warp(&o_full[w], static_cast<uint32_t>(j & 1), &s_abort)) break;
       tc_fence_after();
       float o0[32], o1[32], o2[32], o3[32];
@@ -746,8 +749,8 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
 #pragma unroll
         for (int c = 0; c < 16; ++c) {            // output dims 8c .. 8c+7
           const float* ov = c < 4 ? o0 + c * 8 : c < 8 ? o1 + c * 8 - 32 : c < 12 ? o2 + c * 8 - 64 : o3 + c * 8 - 96;
-          __stcs(po + c * 16, make_uint4(pack_bf16(ov[0], ov[1]), pack_bf16(ov[2], ov[3]), pack_bf16(ov[4], ov[5]),
-                                         pack_bf16(ov[6], ov[7])));
+          __stcs(po + c * 16, make_uint4(pack_f16(ov[0], ov[1]), pack_f16(ov[2], ov[3]), pack_f16(ov[4], ov[5]),
+                                         pack_f16(ov[6], ov[7])));
         }
       }
       // a NaN among the V rows that this row sees (the converters took it out)
@@ -765,7 +768,7 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
 
 // ------------------------------------------------------------------ merge
 struct MergeFp8Args {
-  const __nv_bfloat16* part_o;   // [total_q][Hkv][topk][2048], as the tiles' kernel leaves them
+  const __half* part_o;          // [total_q][Hkv][topk][2048], as the tiles' kernel leaves them
   const float2* part_lse;        // [total_q][Hkv][topk][16 heads]
   const int32_t* block_idx;      // [total_q][Hkv][topk]
   const int32_t* q_start;
@@ -813,10 +816,11 @@ __global__ void __launch_bounds__(256, 6) attn_merge_fp8_kernel(const MergeFp8Ar
       if (w[k] == -INFINITY) continue;
       const float e = exp2f(w[k] - mx), f = e * s_f[s0 + k][h];
       wsum += e;
-      acc[0] = fmaf(f, bf16lo(o[k].x), acc[0]); acc[1] = fmaf(f, bf16hi(o[k].x), acc[1]);
-      acc[2] = fmaf(f, bf16lo(o[k].y), acc[2]); acc[3] = fmaf(f, bf16hi(o[k].y), acc[3]);
-      acc[4] = fmaf(f, bf16lo(o[k].z), acc[4]); acc[5] = fmaf(f, bf16hi(o[k].z), acc[5]);
-      acc[6] = fmaf(f, bf16lo(o[k].w), acc[6]); acc[7] = fmaf(f, bf16hi(o[k].w), acc[7]);
+      float2 v;
+      v = __half22float2(*reinterpret_cast<const __half2*>(&o[k].x)); acc[0] = fmaf(f, v.x, acc[0]); acc[1] = fmaf(f, v.y, acc[1]);
+      v = __half22float2(*reinterpret_cast<const __half2*>(&o[k].y)); acc[2] = fmaf(f, v.x, acc[2]); acc[3] = fmaf(f, v.y, acc[3]);
+      v = __half22float2(*reinterpret_cast<const __half2*>(&o[k].z)); acc[4] = fmaf(f, v.x, acc[4]); acc[5] = fmaf(f, v.y, acc[5]);
+      v = __half22float2(*reinterpret_cast<const __half2*>(&o[k].w)); acc[6] = fmaf(f, v.x, acc[6]); acc[7] = fmaf(f, v.y, acc[7]);
     }
   }
   const float inv = wsum == 0.f ? 0.f : 1.f / wsum;

@@ -1001,7 +1001,7 @@ msa_status_t msa_attn_prefill_fp8(const msa_config_t* cfg, const msa_batch_t* ba
   a.starts = s.starts;
   a.k_cache = static_cast<const uint8_t*>(k_cache_e4m3);
   a.v_cache = static_cast<const uint8_t*>(v_cache_e4m3);
-  a.part_o = reinterpret_cast<__nv_bfloat16*>(ws + w.part_o);
+  a.part_o = reinterpret_cast<__half*>(ws + w.part_o);
   a.part_lse = s.part_lse;
   a.Hq = Hq;
   a.Hkv = Hkv;
@@ -1010,7 +1010,7 @@ msa_status_t msa_attn_prefill_fp8(const msa_config_t* cfg, const msa_batch_t* ba
   CUDA_TRY(set_smem(msa::attn_prefill_fp8_kernel, msa::ATP8_SMEM));
   CUDA_TRY(launch_overlapped(msa::attn_prefill_fp8_kernel, sms, msa::ATP8_THREADS, msa::ATP8_SMEM, stream, tq, a));
   msa::MergeFp8Args m{};
-  m.part_o = reinterpret_cast<const __nv_bfloat16*>(ws + w.part_o);
+  m.part_o = reinterpret_cast<const __half*>(ws + w.part_o);
   m.part_lse = s.part_lse;
   m.block_idx = block_idx;
   m.q_start = batch->q_start;
