@@ -138,8 +138,8 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) 
 // ------------------------------------------------------------------ schedule
 // An entry is a (row t, group g, slot) with a block; its bucket is (window of rows, sequence, g, block).  A window is
 // 8192 rows: one group's queries of that many rows (32 MiB) stay in L2 while its blocks gather them again and again,
-// those of 16,384 rows do not (the last 128K chunk 2.94 ms without windows, 2.84 with, 2.93 with 4096 rows).  Three kernels turn the
-// entries into tiles of up to 8 of a bucket:
+// those of 16,384 rows do not (the last 128K chunk 2.94 ms without windows, 2.84 with, 2.93 with 4096 rows).  Three
+// kernels turn the entries into tiles of up to 8 of a bucket:
 //   count  every entry's bucket and rank in it (a counter per bucket)
 //   bases  every bucket's run of tiles, ceil(count / 8) of them, and its stretch of cost
 //   place  every entry to tile base + rank / 8, place rank % 8; the first of a tile writes the tile's head, and the

@@ -180,6 +180,24 @@ def test_a_block_selected_twice_counts_twice(cuda_ok, which):
 
 
 @pytest.mark.parametrize("which", FORMS)
+@pytest.mark.parametrize("q_size", [0.0, 1.0, 300.0, 3e4])
+def test_largest_values_under_equal_scores(cuda_ok, which, q_size):
+    """Every code is the largest one and every key of a row the same: 128 equal probabilities a block, and logits up to
+    2^21.  The output is 448 v_scale for any weights; the weights' roundings (8 bits, 2^-8), a partial's (2^-8) and the output's
+    (2^-8) move it by less than 2^-6 of itself."""
+    c = Case(41, ctx=[400, 257], nq=[3, 2], which=which)
+    c.k[:] = 0x7E
+    c.v[:] = 0x7E
+    c.ks[:] = 2.0 ** -6
+    c.vs[:] = 2.0 ** -7
+    c.q = torch.full_like(c.q, q_size)
+    out, lse = c.run()
+    assert msa.device_status() == msa.MSA_OK
+    assert ((out[:c.rows].float() - 3.5).abs() <= 3.5 * 2.0 ** -6).all(), (float(out.min()), float(out.max()))
+    assert torch.isfinite(lse[:c.rows]).all()
+
+
+@pytest.mark.parametrize("which", FORMS)
 @pytest.mark.parametrize("q_size", [1e-30, 1e-3, 4.0])
 def test_query_sizes(cuda_ok, which, q_size):
     """Queries from tiny to large, a head of zeros, elements 2^-12 below their head's largest."""
