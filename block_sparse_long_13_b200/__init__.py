@@ -57,7 +57,7 @@ class _CBatch(ctypes.Structure):
 
 
 _lib_handle = None
-# _bind.so, once the library is loaded: these calls' checks and the call itself, natively.  A function of it answers None
+# _bind.so, once the first of these calls is made: their checks and the call itself, natively.  A function of it answers None
 # for arguments that do not fit; the Python code behind each use then says what is wrong with them.
 _calls = None
 _BOUND = ("msa_attn_decode_fp8", "msa_attn_prefill_fp8", "msa_qknorm_rope_insert_fp8", "msa_advance_batch")
@@ -109,15 +109,23 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         getattr(lib, name).restype = ctypes.c_size_t
     lib.msa_status_string.restype = ctypes.c_char_p
     lib.msa_last_error.restype = ctypes.c_char_p
-    global _calls
-    try:
-        from . import _bind
-    except ImportError as e:
-        raise RuntimeError("_bind.so is missing or does not fit this torch: build it with "
-                           "`python -m block_sparse_long_13_b200.build --force`") from e
-    _bind.setup(*(ctypes.cast(getattr(lib, name), P).value for name in _BOUND))
-    _calls, _lib_handle = _bind, lib
+    _lib_handle = lib
     return lib
+
+
+def _native():
+    """_bind.so over the loaded library; raises if it is missing."""
+    global _calls
+    if _calls is None:
+        lib = load_library()
+        try:
+            from . import _bind
+        except ImportError as e:
+            raise RuntimeError("_bind.so is missing or does not fit this torch: build it with "
+                               "`python -m block_sparse_long_13_b200.build --force`") from e
+        _bind.setup(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in _BOUND))
+        _calls = _bind
+    return _calls
 
 
 def _check(status: int) -> None:
@@ -345,8 +353,8 @@ def decode_fp8_workspace_bytes(cfg: Config, batch: Batch) -> int:
 
 
 def _attn_fp8(prefill, cfg, batch, q, k_cache, v_cache, k_scale, v_scale, block_idx, out, lse, workspace, stream):
-    lib = _lib_handle or load_library()
-    status = _calls.attn(prefill, cfg, batch, q, k_cache, v_cache, k_scale, v_scale, block_idx, out, lse, workspace, stream)
+    status = (_calls or _native()).attn(prefill, cfg, batch, q, k_cache, v_cache, k_scale, v_scale, block_idx, out, lse,
+                                        workspace, stream)
     if status is None:
         rows = (batch.total_q, cfg.num_q_heads)
         bf16, heads = torch.bfloat16, rows + (cfg.head_dim,)
@@ -355,6 +363,7 @@ def _attn_fp8(prefill, cfg, batch, q, k_cache, v_cache, k_scale, v_scale, block_
                          (block_idx, torch.int32, (batch.total_q, cfg.num_kv_heads, cfg.topk), "block_idx"),
                          (out, bf16, heads, "out"), (lse, torch.float32, rows, "lse"),
                          (workspace, torch.uint8, (nbytes,), "workspace"), *_batch_arrays(batch))
+        lib = load_library()
         fn = lib.msa_attn_prefill_fp8 if prefill else lib.msa_attn_decode_fp8
         status = fn(cfg._c(), batch._c(host_only=True), *ptrs[:9], nbytes, _stream_here(stream))
     if status:
@@ -379,9 +388,8 @@ def qknorm_rope_insert_fp8(cfg: Config, batch: Batch, q, k_new, v_new, q_norm_w,
                            eps: float = 1e-6, stream=None) -> None:
     """qknorm_rope_insert into an 8-bit cache (see include/msa.h): the queries go to q_out (q itself or another
     buffer), the new rows become codes, and the scales of their pages follow."""
-    lib = _lib_handle or load_library()
-    status = _calls.insert(cfg, batch, q, k_new, v_new, q_norm_w, k_norm_w, q_out, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale,
-                          rotary_dim, rope_theta, eps, stream)
+    status = (_calls or _native()).insert(cfg, batch, q, k_new, v_new, q_norm_w, k_norm_w, q_out, k_cache_e4m3,
+                                          v_cache_e4m3, k_scale, v_scale, rotary_dim, rope_theta, eps, stream)
     if status is None:
         bf16, heads = torch.bfloat16, (batch.total_q, cfg.num_q_heads, cfg.head_dim)
         new = (batch.total_q, cfg.num_kv_heads, cfg.head_dim)
@@ -389,8 +397,9 @@ def qknorm_rope_insert_fp8(cfg: Config, batch: Batch, q, k_new, v_new, q_norm_w,
                          (q_norm_w, bf16, new[2:], "q_norm_w"), (k_norm_w, bf16, new[2:], "k_norm_w"),
                          (q_out, bf16, heads, "q_out"),
                          *_fp8_cache(cfg, batch, k_cache_e4m3, v_cache_e4m3, k_scale, v_scale), *_batch_arrays(batch))
-        status = lib.msa_qknorm_rope_insert_fp8(cfg._c(), batch._c(host_only=True), *ptrs[:10], int(rotary_dim),
-                                                float(rope_theta), float(eps), _stream_here(stream))
+        status = load_library().msa_qknorm_rope_insert_fp8(cfg._c(), batch._c(host_only=True), *ptrs[:10],
+                                                           int(rotary_dim), float(rope_theta), float(eps),
+                                                           _stream_here(stream))
     if status:
         _check(status)
 
@@ -401,9 +410,8 @@ def advance_batch(delta, ctx_len, page_table, free_ring, pool, ctx_len_out, pool
     given back to the ring, and ctx_len_out, q_start and page_table then serve as a Batch.  ctx_len_out may be ctx_len
     and pool_out may be pool.  All tensors int32; nothing is read back to the host: pool_out[2] says on the device how
     many pages the step lacked (0: done, -1: arguments that do not fit)."""
-    lib = _lib_handle or load_library()
-    status = _calls.advance(delta, ctx_len, page_table, free_ring, pool, ctx_len_out, pool_out, q_start, slot_map, block_size,
-                           stream)
+    status = (_calls or _native()).advance(delta, ctx_len, page_table, free_ring, pool, ctx_len_out, pool_out, q_start,
+                                           slot_map, block_size, stream)
     if status is None:
         if page_table.dim() != 2:
             raise MsaError(MSA_ERR_INVALID_ARG, "page_table must be [num_seqs][max_blocks_per_seq]")
@@ -416,7 +424,7 @@ def advance_batch(delta, ctx_len, page_table, free_ring, pool, ctx_len_out, pool
                          (q_start, i32, (n + 1,), "q_start"), (slot_map, i32, (rows,), "slot_map"))
         if rows == 0:
             ptrs[8] = 0                    # an empty slot map is none
-        status = lib.msa_advance_batch(n, width, pages, int(block_size), *ptrs, rows, _stream_here(stream))
+        status = load_library().msa_advance_batch(n, width, pages, int(block_size), *ptrs, rows, _stream_here(stream))
     if status:
         _check(status)
 

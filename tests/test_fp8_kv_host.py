@@ -160,24 +160,24 @@ def test_native_calls_leave_what_does_not_fit_to_python(lib):
     before = [sys.getrefcount(x) for x in held[:-1]]
     ints = [torch.zeros(n, dtype=torch.int32) for n in (2, 2, 8, 4, 2, 4, 3)]
     for _ in range(50):
-        assert msa._calls.attn(False, cfg, b, *args) is None
-        assert msa._calls.attn(True, cfg, b, *args) is None
-        assert msa._calls.attn(False, None, b, *args) is None
-        assert msa._calls.attn(False, cfg, "batch", *args) is None
-        assert msa._calls.attn(False, cfg, b) is None
+        assert msa._native().attn(False, cfg, b, *args) is None
+        assert msa._native().attn(True, cfg, b, *args) is None
+        assert msa._native().attn(False, None, b, *args) is None
+        assert msa._native().attn(False, cfg, "batch", *args) is None
+        assert msa._native().attn(False, cfg, b) is None
         for i in range(len(args)):
-            assert msa._calls.attn(False, cfg, b, *args[:i], object(), *args[i + 1:]) is None
-        assert msa._calls.attn(False, msa.Config(num_q_heads=1 << 40), b, *args) is None
-        assert msa._calls.attn(False, msa.Config(softmax_scale="1"), b, *args) is None
-        assert msa._calls.insert(cfg, b, *args[:4], args[3], args[3], args[0], *args[1:5], 64, 1e4, 1e-6, None) is None
-        assert msa._calls.advance(*ints[:2], torch.zeros(2, 4, dtype=torch.int32), *ints[2:], None, 128, None) is None
-        assert msa._calls.advance(*ints[:2], ints[2], *ints[2:], None, 128, None) is None
-        assert msa._calls.advance() is None
+            assert msa._native().attn(False, cfg, b, *args[:i], object(), *args[i + 1:]) is None
+        assert msa._native().attn(False, msa.Config(num_q_heads=1 << 40), b, *args) is None
+        assert msa._native().attn(False, msa.Config(softmax_scale="1"), b, *args) is None
+        assert msa._native().insert(cfg, b, *args[:4], args[3], args[3], args[0], *args[1:5], 64, 1e4, 1e-6, None) is None
+        assert msa._native().advance(*ints[:2], torch.zeros(2, 4, dtype=torch.int32), *ints[2:], None, 128, None) is None
+        assert msa._native().advance(*ints[:2], ints[2], *ints[2:], None, 128, None) is None
+        assert msa._native().advance() is None
     assert [sys.getrefcount(x) for x in held[:-1]] == before
     with pytest.raises(TypeError):
-        msa._calls.setup(1, 2)
+        msa._native().setup(1, 2)
     with pytest.raises((TypeError, ValueError)):
-        msa._calls.setup(0, 0, 0, 0)
+        msa._native().setup(0, 0, 0, 0)
 
 
 def test_binding_refuses_another_device(lib, monkeypatch):

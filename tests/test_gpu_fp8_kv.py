@@ -15,6 +15,8 @@ step: bf16 2^-8, e4m3 2^-4, relative to the value):
 * a code is off by half a step, 2^-4 of the value or 2^-10 of the scale (below
   the codes' normal range), on top of fp32 arithmetic (1e-5).
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -315,6 +317,34 @@ def test_same_bits_again_on_other_pages_and_another_stream(cuda_ok, which):
     assert msa.device_status() == msa.MSA_OK
     for x in (b, e, f):
         assert torch.equal(a[0], x[0]) and torch.equal(a[1], x[1])
+
+
+@pytest.mark.parametrize("which", FORMS)
+def test_two_threads_call_at_once(cuda_ok, which):
+    """Each on a stream and with a workspace of its own; the interpreter's lock is not held inside the call."""
+    cases = [Case(51 + i, ctx=[700, 40], nq=[3, 1], which=which) for i in range(2)]
+    want = [c.run() for c in cases]
+    torch.cuda.synchronize()
+    got, wrong = [[], []], []
+
+    def work(i):
+        try:
+            side = torch.cuda.Stream()
+            with torch.cuda.stream(side):
+                got[i] = [cases[i].run() for _ in range(10)]
+            side.synchronize()
+        except Exception as e:  # noqa: BLE001
+            wrong.append(e)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+    assert msa.device_status() == msa.MSA_OK
+    for i in range(2):
+        for out, lse in got[i]:
+            assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
 
 
 def test_forms_of_the_arguments(cuda_ok):
