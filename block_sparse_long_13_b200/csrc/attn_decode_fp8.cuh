@@ -8,17 +8,22 @@
 // The codes go from TMA straight into the tensor cores: both products run as kind::f8f6f4 MMAs in the
 // transposed form ("swap AB": a row has only 16 query heads),
 //   S^T = K_b Q^T   (M = 128 keys, N = 16 heads, K = 128 dims),   O_b^T = V_b^T P^T   (M = 128 dims, K = 128 keys),
-// which want Q and P in 8 bits too.  Neither is rounded to 8 bits: each is the sum of two e4m3 numbers, high and
-// low part, multiplied one after the other into the same fp32 accumulator.
-//   Q: scaled per head by a power of two so that the largest |q| is in (224, 448].  A bf16 number has 8
+// which want Q and P in 8 bits too.  Neither is rounded to 8 bits: each is the sum of a few 8-bit numbers, which are
+// columns of one operand and whose products are added in fp32.
+//   Q is the sum of two e4m3 numbers, scaled per head by a power of two so that the largest |q| is in (224, 448].  A bf16 number has 8
 //      significant bits; the high part takes 4 of them, and the rest is a multiple of q's last bit by at most 8
 //      of them either way, which 4 bits hold: exact, down to elements 2^-11 below the head's largest (below it
 //      the error is 2^-10 of a scaled unit, at most 2^-17 of the largest element).
-//   P: 256 2^(x - M) <= 256, rounded first to f16 (2^-12 of itself), then high + low: 2^-9 of itself, 2^-18 of the
-//      row's largest at least.  That is what bf16 probabilities (2^-9) lose, and the sum of probabilities is
-//      taken from the unrounded fp32 values.
+//   P is the sum of three e5m2 numbers (3 significant bits each; the exponents of f16): 2^15 2^(x - m) <= 2^15, m the
+//      block's own maximum, as f16 h; then h = p1 + p2 / 8 + p3 / 64, each part the rest of those before it, rounded.  The rests
+//      are exact in f16, and the factors 8 and 64 keep them above e5m2's least number for as long as h is normal:
+//      off by 2^-11 of itself (f16's 2^-12 included: 2^-10.4) down to probabilities of 2^-29 of the block's largest, by 2^-38
+//      of the block's largest below.  A row may put nearly all its weight on one key whose value is near 0 (a sink): its
+//      output is then made of the small ones, so what counts is their own size, not the largest one's.  Two e4m3 parts under
+//      the row's running maximum, which end at 2^-18 of it, lost a quarter of such an output 12 nats below the sink and all of it from 13.
+//      The sum of probabilities is taken from the unrounded fp32 values.
 // Converting the tiles to 16 bits in shared memory instead would read and write 96 KiB of it a block and
-// keep a warpgroup busy; the second MMA of each pair costs 32 KiB of reads by the tensor core.
+// keep a warpgroup busy.
 //
 // Bound by HBM: 32 KiB a block and group.  148 persistent CTAs, one per SM; each takes an equal run of the
 // rows x groups x topk slots, so that every CTA streams the same number of blocks whatever the batch (whole rows per
@@ -30,14 +35,15 @@
 // one barrier a block (a wait for a barrier that is ready takes about 100 clocks, measured, and a block has 1,400).
 // Warps: 3 looks up slots (32 at a time: block id, sequence, page, scales) and splits the queries, 0 issues the copies,
 // 1 the MMAs of S^T, 2 those of O^T; 4-7 and 12-15 run the softmax on alternate blocks (thread = key; each group keeps
-// the running maxima of its own blocks of the row, so a block's probabilities have the scale of the row so far), 8-11
-// keep the output of either group's blocks (thread = dim): acc = acc 2^(M_old - M) + vs_b O_b.  The chain of a block's
+// the running maxima M of its own blocks of the row), 8-11
+// keep the output of either group's blocks (thread = dim): acc = acc 2^(M_old - M) + vs_b 2^(m - M) O_b.  The chain of a block's
 // softmax is longer than the 0.74 us that its 32 KiB take at the copy bandwidth: hence two groups.  An MMA as
-// narrow as these takes 47 clocks whatever its N (measured, N <= 64), so the high and low parts are the two halves of
-// one N = 32 operand, and the halves of the result are added when it is read.  Every wait is bounded.
-// Measured: 64 rows over 128K keys, 16 blocks, 4 groups: 28.3 us with the merge (134 MB of codes: 4.8 TB/s), of which 20 us
-// are the stream (0.65 us a block and CTA) and 8 set-up, first look-ups, first pass through the code and merge; one row over
-// 32K 10.2 us; 32 x 4 verify rows 49.4 us.  Before the roles shared one barrier a slot the 64 rows took 45.7 us.
+// narrow as these takes 47 clocks whatever its N (measured, N <= 64), so the parts are the 16-wide pieces of
+// one operand (N = 32 and 48), and the pieces of the result are added when it is read.  Every wait is bounded.
+// Measured: 64 rows over 128K keys, 16 blocks, 4 groups: 29.1 us with the merge (134 MB of codes: 4.6 TB/s), of which 21 us
+// are the stream and 8 set-up, first look-ups, first pass through the code and merge; one row over 32K 10.3 us; 32 x 4
+// verify rows 51.7 us.  Three parts of P instead of two, and the factor 2^(m - M), cost 1.1 and 2.7 us of that, half of it in the
+// softmax and half in the output warps; parts by truncation, or a factor for distant blocks only, changed nothing.
 #pragma once
 #include "attn_decode.cuh"
 #include "e4m3.cuh"
@@ -49,11 +55,13 @@ constexpr int ATD8_THREADS = 512;
 constexpr int ATD8_GRID = 148;         // CTAs at most
 constexpr int ATD8_SLOTS = 5;
 constexpr int ATD8_TILE = 16384;       // one K or V block: [128 keys][128 dims] codes, 128-byte swizzle
-constexpr int ATD8_PT = 4096;          // P^T: [16 groups of 8 keys][high, low][8 keys][16 heads]; Q: [high, low][16 heads][128]
+constexpr int ATD8_QT = 4096;          // Q: [high, low][16 heads][128]
+constexpr int ATD8_PT = 6144;          // P^T: [16 groups of 8 keys][3 parts][8 keys][16 heads]
 constexpr int ATD8_BATCHES = 4;        // slot records in flight, 32 each
-constexpr int ATD8_SMEM = ATD8_SLOTS * (2 * ATD8_TILE + ATD8_PT) + 2 * ATD8_PT + 1024;
-constexpr uint32_t ATD8_TM_S = 0, ATD8_TM_O = ATD8_SLOTS * 32, ATD8_TMEM = 512;   // 32 columns each: high, low part
+constexpr int ATD8_SMEM = ATD8_SLOTS * (2 * ATD8_TILE + ATD8_PT) + 2 * ATD8_QT + 1024;
+constexpr uint32_t ATD8_TM_S = 0, ATD8_TM_O = ATD8_SLOTS * 32, ATD8_TMEM = 512;   // 32 and 64 columns each: 16 a part
 constexpr int ATD8_PART = 16 * 128 + 32;   // floats of a partial result: sums [16][128], maxima [16], sums of p [16]
+constexpr float ATD8_PLOG = 15.f, ATD8_PINV = 0x1p-15f;   // a block's probabilities are held times 2^15
 constexpr float ATD8_LOW = -1e30f;     // start of the running maxima (finite: -inf - -inf is NaN)
 
 struct AttnDecodeFp8Args {
@@ -77,12 +85,12 @@ struct AttnDecodeFp8Args {
 // first slot of CTA c
 __device__ __forceinline__ int atd8_first(const AttnDecodeFp8Args& a, int c) { return c * a.per + min(c, a.extra); }
 
-// kind::f8f6f4 with e4m3 operands, fp32 accumulate
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn_major, bool b_mn_major) {
-  return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
+// kind::f8f6f4, A e4m3, B e4m3 or e5m2, fp32 accumulate
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn_major, bool b_mn_major, bool b_e5m2 = false) {
+  return (1u << 4) | ((b_e5m2 ? 1u : 0u) << 10) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
-__device__ __forceinline__ void umma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+__device__ __forceinline__ void umma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                              uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -91,10 +99,10 @@ __device__ __forceinline__ void umma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, u
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// descriptor of P^T, an unswizzled MN-major 8-bit operand of two 16-wide halves: 8 x 16 byte core matrices, the halves
-// 128 bytes and the groups of 8 keys 256 bytes apart
+// descriptor of P^T, an unswizzled MN-major 8-bit operand of three 16-wide parts: 8 x 16 byte core matrices, the parts
+// 128 bytes and the groups of 8 keys 384 bytes apart
 __device__ __forceinline__ uint64_t sdesc_pt(uint32_t saddr) {
-  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(256 >> 4) << 16) |
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(384 >> 4) << 16) |
          (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
 }
 
@@ -131,6 +139,23 @@ __device__ __forceinline__ void e4m3x2_split(float a, float b, uint32_t& hi, uin
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(v) : "r"(d));
   hi = u;
   lo = v;
+}
+
+// Two values (0 .. 2^15) as three pairs of e5m2 numbers, a = a1 + a2 / 8 + a3 / 64: an e5m2 number is the upper byte of an f16
+// one, so the first two pairs are left there (their lower bytes are 0), and half a step added to the bits rounds to it.  A NaN
+// (0x7FFF) loses itself in that sum but not in the rests, and arrives in the third part.
+__device__ __forceinline__ void e5m2x2_split(float a, float b, uint32_t& p1, uint32_t& p2, uint32_t& p3) {
+  uint32_t h, d;
+  uint16_t u;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(b), "f"(a));
+  p1 = (h + 0x00800080u) & 0xFF00FF00u;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(h), "r"(p1));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(h) : "r"(d), "r"(0x48004800u));   // 8
+  p2 = (h + 0x00800080u) & 0xFF00FF00u;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(h), "r"(p2));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(h) : "r"(d), "r"(0x48004800u));
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(u) : "r"(h));
+  p3 = u;
 }
 
 // A head's queries come to (224, 448] times 2^k, 448 = 1.75 * 2^8, by the largest of them (|q| as bf16 bits: NaN above
@@ -178,7 +203,7 @@ attn_decode_fp8_kernel(const __grid_constant__ CUtensorMap tmap_k,    // k codes
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dsmem) + 1023) & ~uintptr_t(1023));
   uint8_t* tiles = smem;                                  // slots of [K 16 KiB][V 16 KiB]
   uint8_t* q_s = tiles + ATD8_SLOTS * 2 * ATD8_TILE;      // 2 x [high, low][16 heads][128] (128-byte swizzle)
-  uint8_t* p_s = q_s + 2 * ATD8_PT;                       // slots of P^T
+  uint8_t* p_s = q_s + 2 * ATD8_QT;                       // slots of P^T
 
   // Of a slot: kv_full its tiles are there; s_full S^T is in TMEM; p_full P^T and the factors are in shared memory;
   // o_full O^T is in TMEM; o_empty O^T and the factors are read.
@@ -189,8 +214,8 @@ attn_decode_fp8_kernel(const __grid_constant__ CUtensorMap tmap_k,    // k codes
   __shared__ uint32_t s_mask[ATD8_BATCHES];               // slots of the batch that hold a block
   __shared__ __align__(16) float s_fq[2][16];             // softmax scale x log2 e / the query's power of two
   __shared__ __align__(16) float s_red[2][2][4][16];      // per softmax group: the warps' maxima of a block, by parity
-  __shared__ __align__(16) float s_run[8][2][16];         // per softmax warp: running maxima, the block's factors
-  __shared__ __align__(16) float s_alpha[ATD8_SLOTS][16]; // 2^(M_old - M) of a block
+  __shared__ __align__(16) float s_run[8][3][16];         // per softmax warp: a block's maxima m, 2^(M_old - M), 2^(m - M - 15)
+  __shared__ __align__(16) float s_fac[ATD8_SLOTS][2][16];   // 2^(M_old - M) and 2^(m - M) of a block
   __shared__ __align__(16) float s_m[2][2][16], s_l[2][8][16];   // of a finished (row, group): maxima, sums of p per warp
   __shared__ __align__(16) float s_fin[4][2][16];         // per output warp: what the two groups' sums are weighted by
   __shared__ uint32_t s_tmem;
@@ -330,7 +355,7 @@ attn_decode_fp8_kernel(const __grid_constant__ CUtensorMap tmap_k,    // k codes
         if (!mbar_wait_soon_warp(&q_empty[qb], ((u >> 1) & 1) ^ 1, &s_abort)) { bt = nbatch; break; }
         if (half == 0) s_fq[qb][h] = query_factor(m, a.scale_log2);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) split_queries(q_s + qb * ATD8_PT, h, half * 64 + i * 16, x[2 * i], x[2 * i + 1], mult);
+        for (int i = 0; i < 4; ++i) split_queries(q_s + qb * ATD8_QT, h, half * 64 + i * 16, x[2 * i], x[2 * i + 1], mult);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[qb]);
@@ -393,10 +418,10 @@ attn_decode_fp8_kernel(const __grid_constant__ CUtensorMap tmap_k,    // k codes
           if (!mbar_wait_soon(&kv_full[st], ph, &s_abort)) { ok = false; break; }
           tc_fence_after();
           if (lane == 0) {
-            const uint64_t kd = k_d + ((st * 2 * ATD8_TILE) >> 4), qd = q_d + (((u & 1) * ATD8_PT) >> 4);
+            const uint64_t kd = k_d + ((st * 2 * ATD8_TILE) >> 4), qd = q_d + (((u & 1) * ATD8_QT) >> 4);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)   // 32 dims per step, within a 128-byte row
-              umma_e4m3_ss(tmem + ATD8_TM_S + st * 32, kd + kk * 2, qd + kk * 2, id_s, kk > 0 ? 1u : 0u);
+              umma_f8_ss(tmem + ATD8_TM_S + st * 32, kd + kk * 2, qd + kk * 2, id_s, kk > 0 ? 1u : 0u);
             umma_commit(&s_full[st]);
           }
           if (++st == ATD8_SLOTS) { st = 0; ph ^= 1; }
@@ -416,7 +441,7 @@ attn_decode_fp8_kernel(const __grid_constant__ CUtensorMap tmap_k,    // k codes
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------ O_b^T = V_b^T P^T; lane 0 issues
-    const uint32_t id_pv = idesc_e4m3(128, 32, true, true);    // A = V_b^T, B = P^T (both MN-major)
+    const uint32_t id_pv = idesc_e4m3(128, 48, true, true, true);   // A = V_b^T, B = P^T in e5m2 (both MN-major)
     const uint64_t v_d = sdesc_sw128(smem_u32(tiles) + ATD8_TILE, ATD8_TILE, 1024);
     const uint64_t p_d = sdesc_pt(smem_u32(p_s));
     int st = 0, ph = 0;
@@ -431,8 +456,8 @@ attn_decode_fp8_kernel(const __grid_constant__ CUtensorMap tmap_k,    // k codes
         if (lane == 0) {
           const uint64_t vd = v_d + ((st * 2 * ATD8_TILE) >> 4), pd = p_d + ((st * ATD8_PT) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)     // 32 keys per step: 4 KiB of V rows, 1 KiB of P rows
-            umma_e4m3_ss(tmem + ATD8_TM_O + st * 32, vd + kk * 256, pd + kk * 64, id_pv, kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < 4; ++kk)     // 32 keys per step: 4 KiB of V rows, 1.5 KiB of P rows
+            umma_f8_ss(tmem + ATD8_TM_O + st * 64, vd + kk * 256, pd + kk * 96, id_pv, kk > 0 ? 1u : 0u);
           umma_commit(&o_full[st]);
         }
         if (++st == ATD8_SLOTS) { st = 0; ph ^= 1; }
@@ -503,14 +528,18 @@ attn_decode_fp8_kernel(const __grid_constant__ CUtensorMap tmap_k,    // k codes
           }
           if (named_bar_any(1 + grp, 128, !ok)) { met = true; break; }
           // every warp joins the four maxima for itself, a head per lane, and hands them to its lanes
-          const float bm = fmaxf(fmaxf(red[0][h16], red[1][h16]), fmaxf(red[2][h16], red[3][h16]));
+          const float bm = fmaxf(fmaxf(fmaxf(red[0][h16], red[1][h16]), fmaxf(red[2][h16], red[3][h16])), ATD8_LOW);
           const float old = mine;
           mine = fmaxf(old, bm);
-          const float fac = exp2f(old - mine);
+          const float fac = exp2f(old - mine), rel = exp2f(bm - mine);
           if (lane < 16) {
-            s_run[w8][0][lane] = mine;
+            s_run[w8][0][lane] = bm;
             s_run[w8][1][lane] = fac;
-            if (sw == 0) s_alpha[st][lane] = fac;
+            s_run[w8][2][lane] = rel * ATD8_PINV;
+            if (sw == 0) {
+              s_fac[st][0][lane] = fac;
+              s_fac[st][1][lane] = rel;
+            }
           }
           if (__any_sync(0xFFFFFFFFu, mine > old)) {
 #pragma unroll
@@ -520,26 +549,29 @@ attn_decode_fp8_kernel(const __grid_constant__ CUtensorMap tmap_k,    // k codes
             }
           }
           __syncwarp();
-          uint32_t hi[4], lw[4];
+          uint32_t p1[4], p2[4], p3[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float4 m = *reinterpret_cast<const float4*>(&s_run[w8][0][4 * i]);
-            const float mm[4] = {m.x, m.y, m.z, m.w};
+            const float4 f = *reinterpret_cast<const float4*>(&s_run[w8][2][4 * i]);
+            const float mm[4] = {m.x, m.y, m.z, m.w}, ff[4] = {f.x, f.y, f.z, f.w};
             float p[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              p[k] = exp2f((x[4 * i + k] - mm[k]) + 8.f);              // 256 2^(x - M); 2^-inf = 0
-              L[4 * i + k] += p[k];
+              p[k] = exp2f((x[4 * i + k] - mm[k]) + ATD8_PLOG);        // 2^15 2^(x - m); 2^-inf = 0
+              L[4 * i + k] = fmaf(p[k], ff[k], L[4 * i + k]);
             }
-            uint32_t h0, l0, h1, l1;
-            e4m3x2_split(p[0], p[1], h0, l0);
-            e4m3x2_split(p[2], p[3], h1, l1);
-            hi[i] = h0 | (h1 << 16);
-            lw[i] = l0 | (l1 << 16);
+            uint32_t a1, a2, a3, b1, b2, b3;
+            e5m2x2_split(p[0], p[1], a1, a2, a3);
+            e5m2x2_split(p[2], p[3], b1, b2, b3);
+            p1[i] = __byte_perm(a1, b1, 0x7531);
+            p2[i] = __byte_perm(a2, b2, 0x7531);
+            p3[i] = a3 | (b3 << 16);
           }
-          uint8_t* pt = p_s + st * ATD8_PT + (row >> 3) * 256 + (row & 7) * 16;
-          *reinterpret_cast<uint4*>(pt) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(pt + 128) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+          uint8_t* pt = p_s + st * ATD8_PT + (row >> 3) * 384 + (row & 7) * 16;
+          *reinterpret_cast<uint4*>(pt) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
+          *reinterpret_cast<uint4*>(pt + 128) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+          *reinterpret_cast<uint4*>(pt + 256) = make_uint4(p3[0], p3[1], p3[2], p3[3]);
           if (nvis < 128) {                  // V rows behind the query may hold NaN codes, and 0 x NaN is NaN
             if (!mbar_wait_soon_warp(&kv_full[st], ph, &s_abort)) { ok = false; break; }
             if (row >= nvis) {
@@ -595,23 +627,29 @@ attn_decode_fp8_kernel(const __grid_constant__ CUtensorMap tmap_k,    // k codes
           const float vs = __int_as_float(__shfl_sync(0xFFFFFFFFu, r.w, j));
           if (!mbar_wait_soon_warp(&o_full[st], ph, &s_abort)) { ok = false; break; }
           tc_fence_after();
-          float o[32], al[16];
-          tmem_ld32(o_addr + st * 32, o);
+          float o[16], o2[16], o3[16], al[16], f[16];
+          tmem_ld16(o_addr + st * 64, o);
+          tmem_ld16(o_addr + st * 64 + 16, o2);
+          tmem_ld16(o_addr + st * 64 + 32, o3);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float4 f = *reinterpret_cast<const float4*>(&s_alpha[st][4 * i]);
-            al[4 * i] = f.x; al[4 * i + 1] = f.y; al[4 * i + 2] = f.z; al[4 * i + 3] = f.w;
+            const float4 x = *reinterpret_cast<const float4*>(&s_fac[st][0][4 * i]);
+            const float4 y = *reinterpret_cast<const float4*>(&s_fac[st][1][4 * i]);
+            al[4 * i] = x.x; al[4 * i + 1] = x.y; al[4 * i + 2] = x.z; al[4 * i + 3] = x.w;
+            f[4 * i] = y.x * vs; f[4 * i + 1] = y.y * vs; f[4 * i + 2] = y.z * vs; f[4 * i + 3] = y.w * vs;
           }
           tmem_ld_wait();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&o_empty[st]);
+#pragma unroll
+          for (int h = 0; h < 16; ++h) o[h] = fmaf(fmaf(o3[h], 0.125f, o2[h]), 0.125f * ATD8_PINV, o[h] * ATD8_PINV);
           if (nb & 1) {
 #pragma unroll
-            for (int h = 0; h < 16; ++h) acc1[h] = fmaf(o[h] + o[16 + h], vs, acc1[h] * al[h]);
+            for (int h = 0; h < 16; ++h) acc1[h] = fmaf(o[h], f[h], acc1[h] * al[h]);
           } else {
 #pragma unroll
-            for (int h = 0; h < 16; ++h) acc0[h] = fmaf(o[h] + o[16 + h], vs, acc0[h] * al[h]);
+            for (int h = 0; h < 16; ++h) acc0[h] = fmaf(o[h], f[h], acc0[h] * al[h]);
           }
           ++nb;
           if (++st == ATD8_SLOTS) { st = 0; ph ^= 1; }
@@ -638,7 +676,7 @@ attn_decode_fp8_kernel(const __grid_constant__ CUtensorMap tmap_k,    // k codes
                 part[2048 + lane] = m;
                 part[2064 + lane] = l;
               } else if (a.lse) {
-                a.lse[head0 + lane] = l == 0.f ? -INFINITY : (m + (log2f(l) - 8.f)) * 0.69314718055994531f;
+                a.lse[head0 + lane] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
               }
             }
           }
@@ -710,7 +748,7 @@ __global__ void __launch_bounds__(128) attn_decode_fp8_merge_kernel(const AttnDe
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const long o = static_cast<long>(t) * a.Hq + g * 16 + h;
   *reinterpret_cast<uint2*>(a.out + o * 128 + d0) = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-  if (a.lse && d0 == 0) a.lse[o] = l == 0.f ? -INFINITY : (M + (log2f(l) - 8.f)) * 0.69314718055994531f;
+  if (a.lse && d0 == 0) a.lse[o] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
 }
 
 }  // namespace msa
