@@ -5,9 +5,11 @@
 // S = Q K^T and O = P V on tcgen05; per-slot partials; log-sum-exp merge), over codes:
 //   x_j = (scale log2 e) ks_b (q . ck_j),   O_b = vs_b sum_j 2^(x_j - m) cv_j / l,   lse_b = (m + log2 l) ln 2.
 // The codes are widened once per (run of tiles, block) by four converter warps, K to bf16 (an MMA's operands have one
-// type, and the queries are bf16) and V to f16 (one conversion instruction for two codes; P is then f16 too, three bits
-// more than bf16 for numbers of at most 1); both hold every e4m3 value.  The scales stay fp32 factors of the softmax
-// and of the output: nothing is rounded that the bf16 form does not round.
+// type, and the queries are bf16) and V to f16, times 2^-15 (P is then f16 too, three bits more than bf16); both hold every
+// e4m3 value.  The scales stay fp32 factors of the softmax and of the output: nothing is rounded that the bf16 form does not
+// round.  P is 2^14 times the probability relative to the block's largest, for which V's 2^-15 makes room: f16 holds it to
+// 2^-12 of itself down to 2^-28 of the largest.  A key of large weight and a value near 0 (a sink) leaves the output to the
+// small ones, and with P at most 1/2 those 15 nats below it were off by 2 % and lost from 17.
 // Feeding the tensor cores with the codes, as the decode form does, would take P in two 8-bit parts, 256 more
 // instructions for each row of 128 keys in the softmax warps that set this kernel's pace; a block's widening is 20 to 45
 // instructions per 16 codes, once for all tokens that selected it, in warps of their own.
@@ -92,13 +94,15 @@ __device__ __forceinline__ void widen16_bf16(uint8_t* tile, int c, const uint4& 
   }
   store16(tile, c, y);
 }
+// V's values times 2^-15
 __device__ __forceinline__ void widen16_f16(uint8_t* tile, int c, const uint4& x) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
   uint32_t y[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y[2 * i]) : "h"(static_cast<uint16_t>(w[i] & 0xFFFFu)));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(y[2 * i + 1]) : "h"(static_cast<uint16_t>(w[i] >> 16)));
+  for (int i = 0; i < 8; ++i) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xFFFFu)));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y[i]) : "r"(h), "r"(0x02000200u));   // exact: multiples of 2^-24, 4 bits
   }
   store16(tile, c, y);
 }
@@ -321,8 +325,9 @@ struct AttnPrefillFp8Args {
   const uint8_t* k_cache;    // [pages][Hkv][128][128] codes
   const uint8_t* v_cache;
   // Partials of (row, group, slot): O is not divided by l and counts codes, as f16 (bf16 would cost no less and take the error
-  // against 64 bits from 1.7e-3, that of the output's own rounding, to 2.3e-3), [16 pieces of 8 dims][16 heads][8], so that a
-  // warp's stores are whole lines; of each head log2(sum) and v_scale / l, the factor that O still wants.
+  // against 64 bits from 1.7e-3, that of the output's own rounding, to 2.3e-3; f16's least step adds at most 2^-24 v_scale, 2^-15
+  // of the least code), [16 pieces of 8 dims][16 heads][8], so that a
+  // warp's stores are whole lines; of each head log2(sum) and v_scale / sum, the factor that O still wants.
   __half* part_o;            // [total_q][Hkv][topk][2048]
   float2* part_lse;          // [total_q][Hkv][topk][16 heads]
   int Hq, Hkv, topk;
@@ -700,9 +705,9 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
 #pragma unroll
       for (int c = 0; c < 32; ++c) mx[c & 7] = fmax3(mx[c & 7], fmaxf(v0[c], v1[c]), fmaxf(v2[c], v3[c]));
       const float m = fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], fmax3(mx[4], mx[5], mx[6]), mx[7]));
-      // P at most 1/2, so that a sum of 128 codes of 448 stays an f16 number with room for the rounding of m sc; -inf only on
-      // rows past the tile's entries
-      const float mc = (m > -INFINITY) ? fmaf(m, sc, 1.f) : 0.f;
+      // P at most 2^14: with V's 2^-15 that is 1/2, so that a sum of 128 codes of 448 stays an f16 number with room for the
+      // rounding of m sc; -inf only on rows past the tile's entries
+      const float mc = (m > -INFINITY) ? fmaf(m, sc, -14.f) : 0.f;
       // ---- P = exp2(scale * S - max) as f16 pairs into P[w] (TMEM), two halves of 64 keys
       float l0 = 0.f, l1 = 0.f;
       const unsigned long long sc2 = pair(sc, sc), mc2 = pair(-mc, -mc);
@@ -755,7 +760,7 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
       }
       // a NaN among the V rows that this row sees (the converters took it out)
       const int4 vn = *reinterpret_cast<const int4*>(s_vnan[nbucket & 3]);
-      const float inv = min(min(vn.x, vn.y), min(vn.z, vn.w)) < vis ? __uint_as_float(0x7FC00000u) : vs / l;
+      const float inv = min(min(vn.x, vn.y), min(vn.z, vn.w)) < vis ? __uint_as_float(0x7FC00000u) : vs / (l * 0x1p-15f);
       if (valid) a.part_lse[part * ATTP_G + h] = make_float2(mc + log2f(l), inv);
     }
   }

@@ -15,7 +15,6 @@ from . import test_gpu_fp8_kv as T
 msa = T.msa
 pytestmark = pytest.mark.gpu
 
-FORMS = ["decode", "prefill"]
 ROWS = {
     "one block": dict(ctx=[100, 128, 77], nq=[1, 1, 2], kv=2, topk=1),
     "16 blocks, one row": dict(ctx=[2100], nq=[1], kv=4, topk=16),
@@ -50,9 +49,9 @@ def sink_case(seed, gap, equal, which, **shape):
     return c
 
 
-@pytest.mark.parametrize("which", FORMS)
+@pytest.mark.parametrize("which", T.FORMS)
 @pytest.mark.parametrize("equal", [False, True], ids=["spread", "equal"])
-@pytest.mark.parametrize("gap", [10, 12, 14, 16, 19])
+@pytest.mark.parametrize("gap", [12, 15, 19])
 @pytest.mark.parametrize("shape", ROWS)
 def test_small_probabilities_under_a_sink(cuda_ok, shape, gap, equal, which):
     c = sink_case(61, gap, equal, which, **ROWS[shape])
@@ -61,7 +60,7 @@ def test_small_probabilities_under_a_sink(cuda_ok, shape, gap, equal, which):
     c.check(out, lse, range(c.main))
 
 
-@pytest.mark.parametrize("which", FORMS)
+@pytest.mark.parametrize("which", T.FORMS)
 def test_a_row_is_as_exact_in_a_batch_as_alone(cuda_ok, which):
     """The same row with its sink, alone and as the last one of a batch (other borders between the CTAs): both within the
     bound of the definition."""
