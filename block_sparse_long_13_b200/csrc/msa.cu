@@ -139,10 +139,16 @@ msa_status_t make_map(CUtensorMap* m, const void* base, int rank, const uint64_t
   return MSA_OK;
 }
 
+// The dynamic shared memory that launches of a kernel may ask for.  It is a property of the kernel, which host threads
+// share: `most` is what any call may want, not this one's size, or a call beside it could lower it between another's setting
+// and launch.
 template <typename K>
-cudaError_t set_smem(K kernel, int bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+cudaError_t set_smem(K kernel, int most) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
 }
+constexpr int kRingBytes = 200 * 1024;         // the indexers' tiles in shared memory, beside 1 KiB of alignment
+constexpr int kMaxKvHeads = 16;                // as many as indexer heads (check_config), with 16 query heads each
+constexpr int kMaxQHeads = 16 * kMaxKvHeads;
 
 msa_status_t launched() {
   cudaError_t e = cudaGetLastError();
@@ -268,11 +274,11 @@ msa_status_t launch_index_prefill(const msa_config_t* cfg, const msa_batch_t* ba
   a.nsplit = FUSED ? 1 : 4;
   const int q_tile = hg * 128 * 64 * 2;
   const int xbuf = FUSED ? 128 * msa::IDXP_FUSED_SLOTS * 8 : 0;   // candidate exchange between warpgroups
-  a.nqbuf = (2 * q_tile + 2 * msa::IDXP_STAGE_BYTES <= 200 * 1024 - xbuf) ? 2 : 1;
-  a.stages = std::min(8, (200 * 1024 - xbuf - a.nqbuf * q_tile) / msa::IDXP_STAGE_BYTES);
+  a.nqbuf = (2 * q_tile + 2 * msa::IDXP_STAGE_BYTES <= kRingBytes - xbuf) ? 2 : 1;
+  a.stages = std::min(8, (kRingBytes - xbuf - a.nqbuf * q_tile) / msa::IDXP_STAGE_BYTES);
   CHECK_SUP(a.stages >= 2, "indexer tiles too large for the shared-memory ring");
   const int smem = a.nqbuf * q_tile + a.stages * msa::IDXP_STAGE_BYTES + xbuf + 1024;
-  CUDA_TRY(set_smem(msa::index_prefill_kernel<FUSED>, smem));
+  CUDA_TRY(set_smem(msa::index_prefill_kernel<FUSED>, kRingBytes + 1024));
   msa::index_prefill_kernel<FUSED><<<sms, msa::IDXP_THREADS, smem, stream>>>(tq, tk, a);
   return launched();
 }
@@ -354,11 +360,11 @@ msa_status_t launch_index_decode(const msa_config_t* cfg, const msa_batch_t* bat
       if ((st = make_map(&tq, idx_q, 3, dims, strides, box)) != MSA_OK) return st;
     }
     const int q_tiles = 2 * Hi * msa::IDXT_QHEAD;
-    a.stages = std::min(16, (200 * 1024 - q_tiles) / a.stage_bytes);
+    a.stages = std::min(16, (kRingBytes - q_tiles) / a.stage_bytes);
     CHECK_SUP(a.stages >= 2, "indexer tiles too large for the shared-memory ring");
     const int smem = a.stages * a.stage_bytes + q_tiles + 1024;
     auto go_tc = [&](auto kernel) -> msa_status_t {
-      CUDA_TRY(set_smem(kernel, smem));
+      CUDA_TRY(set_smem(kernel, kRingBytes + 1024));
       kernel<<<sms, msa::IDXT_THREADS, smem, stream>>>(tk, tq, a);
       return launched();
     };
@@ -371,7 +377,7 @@ msa_status_t launch_index_decode(const msa_config_t* cfg, const msa_batch_t* bat
   CHECK_SUP(a.stages >= 2, "indexer tiles too large for the shared-memory ring");
   const int smem = a.stages * a.stage_bytes + q_bytes + 1024;
   auto go = [&](auto kernel) -> msa_status_t {
-    CUDA_TRY(set_smem(kernel, smem));
+    CUDA_TRY(set_smem(kernel, msa::IDXD_SMEM_BUDGET + 1024));
     kernel<<<sms, msa::idxd_threads(nqb, E4M3), smem, stream>>>(tk, a);
     return launched();
   };
@@ -663,7 +669,7 @@ msa_status_t msa_qknorm_rope_insert(const msa_config_t* cfg, const msa_batch_t* 
   a.log2_theta = std::log2(static_cast<double>(rope_theta));
   a.eps = eps;
   const int smem = msa::qkr_smem_bytes(a.Hq, a.Hkv);
-  CUDA_TRY(set_smem(msa::qk_rope_insert_kernel, smem));
+  CUDA_TRY(set_smem(msa::qk_rope_insert_kernel, msa::qkr_smem_bytes(kMaxQHeads, kMaxKvHeads)));
   // eight CTAs per SM need their shared memory more than L1 (no data is reused)
   CUDA_TRY(cudaFuncSetAttribute(msa::qk_rope_insert_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
                                 cudaSharedmemCarveoutMaxShared));
@@ -1045,7 +1051,6 @@ msa_status_t msa_qknorm_rope_insert_fp8(const msa_config_t* cfg, const msa_batch
   CHECK_ARG(std::isfinite(rope_theta) && rope_theta > 0.f, "rope_theta must be positive and finite");
   CHECK_ARG(std::isfinite(eps) && eps >= 0.f, "eps must be finite and >= 0");
   const int smem = cfg->num_q_heads * msa::QKR_D * 2;
-  CHECK_SUP(smem <= 200 * 1024, "too many query heads");
   CHECK_SUP(static_cast<int64_t>(batch->num_seqs) + batch->total_q < (1LL << 31) / (cfg->num_kv_heads + 1),
             "too many sequences and rows");
   if (batch->total_q == 0) return MSA_OK;
@@ -1090,7 +1095,7 @@ msa_status_t msa_qknorm_rope_insert_fp8(const msa_config_t* cfg, const msa_batch
   qa.rotary_dim = rotary_dim;
   qa.eps = eps;
   const auto q_kernel = batch->total_q > msa::QNR_MANY ? msa::q_norm_rope_kernel<8> : msa::q_norm_rope_kernel<1>;
-  CUDA_TRY(set_smem(q_kernel, smem));
+  CUDA_TRY(set_smem(q_kernel, kMaxQHeads * msa::QKR_D * 2));
   CUDA_TRY(cudaFuncSetAttribute(q_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared));
   CUDA_TRY(launch_overlapped(q_kernel, static_cast<unsigned>(batch->total_q), msa::QKR_THREADS, smem, stream, qa, tab));
   return MSA_OK;
@@ -1128,7 +1133,7 @@ msa_status_t msa_advance_batch(int32_t num_seqs, int32_t max_blocks_per_seq, int
   a.num_pages = num_pages;
   a.max_rows = max_rows;
   const int smem = msa::advance_smem(num_seqs);
-  if (smem > 46 * 1024) CUDA_TRY(set_smem(msa::advance_batch_kernel, smem));   // 48 KiB with the static arrays need no leave
+  if (smem > 46 * 1024) CUDA_TRY(set_smem(msa::advance_batch_kernel, msa::advance_smem(msa::ADV_MAXSEQ)));   // 48 KiB with the static arrays need no leave
   msa::advance_batch_kernel<<<1, msa::ADV_THREADS, smem, stream>>>(a);
   msa_status_t st = launched();
   if (st != MSA_OK || max_rows <= msa::ADV_ONE) return st;
