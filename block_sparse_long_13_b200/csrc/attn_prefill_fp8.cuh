@@ -111,6 +111,21 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// NaN into the dims of a partial (one head's, [16 pieces][16 heads][8 dims]) in which one of the first `keys` V rows has a NaN
+// code.  Slow and rare: the codes once more, out of L2.
+__device__ __forceinline__ void nan_dims(const uint8_t* v, int keys, __half* po) {
+#pragma unroll 1
+  for (int i = 0; i < keys * 8; ++i) {
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(v) + i);
+    if (!has_nan(x)) continue;
+#pragma unroll 1
+    for (int b = 0; b < 16; ++b) {
+      const uint32_t word = b < 8 ? (b < 4 ? x.x : x.y) : (b < 12 ? x.z : x.w);
+      const int d = (i & 7) * 16 + b;
+      if (((word >> (8 * (b & 3))) & 0x7Fu) == 0x7Fu) po[(d >> 3) * 128 + (d & 7)] = __ushort_as_half(0x7FFF);
+    }
+  }
+}
 // two fp32 operations an instruction (the same roundings)
 __device__ __forceinline__ unsigned long long pair(float a, float b) {
   unsigned long long r;
@@ -758,10 +773,16 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
                                          pack_f16(ov[6], ov[7])));
         }
       }
-      // a NaN among the V rows that this row sees (the converters took it out)
-      const int4 vn = *reinterpret_cast<const int4*>(s_vnan[nbucket & 3]);
-      const float inv = min(min(vn.x, vn.y), min(vn.z, vn.w)) < vis ? __uint_as_float(0x7FC00000u) : vs / (l * 0x1p-15f);
-      if (valid) a.part_lse[part * ATTP_G + h] = make_float2(mc + log2f(l), inv);
+      if (valid) {
+        // NaN codes among the V rows that this row sees (the converters took them out): NaN in their dims
+        const int4 vn = *reinterpret_cast<const int4*>(s_vnan[nbucket & 3]);
+        if (min(min(vn.x, vn.y), min(vn.z, vn.w)) < vis) {
+          // this tile's record is still there: tile i + 8's needs this warp's P of tile i + 2
+          const int row = s_rec[(2 * j + w) % ATP8_RECS][0].y;
+          nan_dims(a.v_cache + static_cast<long>(row) * 128, vis, a.part_o + part * 2048 + h * 8);
+        }
+        a.part_lse[part * ATTP_G + h] = make_float2(mc + log2f(l), vs / (l * 0x1p-15f));
+      }
     }
   }
   __syncwarp();

@@ -282,8 +282,9 @@ msa_status_t msa_merge_partials(int32_t n, int64_t units, int32_t head_dim, cons
  * msa_attn_prefill on the values of such a cache, for few and for many queries
  * per sequence (either takes any batch).  Rows whose selection leaves no key
  * (all -1) get out = 0 and lse = -inf; rows t >= q_start[num_seqs] (a batch
- * padded to total_q) are left as they were.  A selected NaN code makes the
- * results of its row NaN.  A selected block whose id or page is out of range is
+ * padded to total_q) are left as they were.  A NaN code in a key that a row
+ * sees makes the row's results NaN for the group's heads; one in a value makes
+ * its own dim of their outputs NaN, and no other and no lse.  A selected block whose id or page is out of range is
  * recorded as MSA_ERR_DEVICE_BOUNDS and left out.  `workspace` must hold
  * msa_decode_fp8_workspace_bytes / msa_prefill_fp8_workspace_bytes bytes;
  * nothing in it needs to be initialised, and calls that may overlap on the GPU

@@ -59,3 +59,23 @@ def test_inserts_of_different_head_counts_at_once(cuda_ok):
             msa.qknorm_rope_insert_fp8(c["cfg"], c["batch"], q, kn, vn, qw, kw, q, k, v, ks, vs)
     _together(work, cases)
     assert msa.device_status() == msa.MSA_OK
+
+
+@pytest.mark.parametrize("which", T.FORMS)
+def test_a_nan_value_reaches_its_own_dim_only(cuda_ok, which):
+    """Single NaN codes in values: rows that see one have NaN in its dim, for every head, and what the others hold
+    elsewhere; lse does not notice."""
+    c = T.Case(72, ctx=[100, 700], nq=[100, 40], which=which, kv=2, topk=6)
+    for s, at, g, dim, code in ((0, 60, 0, 5, 0x7F), (0, 0, 1, 127, 0xFF), (0, 99, 1, 0, 0x7F), (1, 130, 1, 64, 0x7F),
+                                (1, 130, 1, 79, 0xFF), (1, 690, 0, 33, 0xFF)):
+        c.v[c.table[s, at // 128], g, at % 128, dim] = code
+    rows = np.arange(c.main)
+    ref, ref_lse, mag = T.K.attention(c.q[rows].double().numpy(), T.K.values(c.k, c.ks), T.K.values(c.v, c.vs), c.seq[rows],
+                                      c.pos[rows], c.sel[rows], c.table)
+    out, lse = c.run()
+    assert msa.device_status() == msa.MSA_OK
+    got = out[:c.main].double().cpu().numpy()
+    nan = np.isnan(ref)
+    assert 0 < nan.sum() < nan.size // 16 and np.array_equal(np.isnan(got), nan)
+    assert (np.abs(got - ref)[~nan] <= (2.0 ** -8 * np.abs(ref) + (2.0 ** -7 + 2.0 ** -12) * mag)[~nan]).all()
+    assert np.abs(lse[:c.main].cpu().numpy() - ref_lse).max() <= T.LSE_ABS
