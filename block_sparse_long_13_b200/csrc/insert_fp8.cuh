@@ -227,6 +227,8 @@ kv_insert_fp8_kernel(const KvInsertArgs a, const __grid_constant__ RopeTable tab
     if (threadIdx.x == 0) flag_error(MSA_DEV_BOUNDS);
     return -1;
   };
+  // whether rows t0 .. t0 + nq - 1 at positions p0 .. are a sequence of the batch; none of its pieces is written otherwise
+  auto fits = [&](int t0, int nq, int p0) { return p0 >= 0 && t0 >= 0 && t0 + nq <= a.total_q && nq <= a.max_q; };
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rows = min(a.total_q, __ldg(a.q_start + a.num_seqs));
   for (int piece = blockIdx.x; piece < a.pieces; piece += gridDim.x) {
@@ -234,7 +236,7 @@ kv_insert_fp8_kernel(const KvInsertArgs a, const __grid_constant__ RopeTable tab
     if (i < a.num_seqs) {                                // the block that the sequence's first new row falls in
       const int t0 = __ldg(a.q_start + i), nq = __ldg(a.q_start + i + 1) - t0, p0 = __ldg(a.ctx_len + i) - nq;
       if (nq <= 0) continue;
-      if (p0 < 0 || t0 < 0 || t0 + nq > a.total_q || nq > a.max_q) {
+      if (!fits(t0, nq, p0)) {
         if (tid == 0) flag_error(MSA_DEV_BOUNDS);
         continue;
       }
@@ -254,7 +256,7 @@ kv_insert_fp8_kernel(const KvInsertArgs a, const __grid_constant__ RopeTable tab
         const int end = __ldg(a.q_start + s + 1);
         p = __ldg(a.ctx_len + s) - end + t;
         const int first = __ldg(a.q_start + s);
-        lead = t != first && end - first <= a.max_q && p > 0 && (p & 127) == 0;
+        lead = t != first && fits(first, end - first, p - (t - first)) && (p & 127) == 0;
       }
       vote = __ballot_sync(0xFFFFFFFFu, lead);
       if (lane == 0) s_cnt[warp] = __popc(vote);

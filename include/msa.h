@@ -317,8 +317,8 @@ msa_status_t msa_attn_prefill_fp8(const msa_config_t* cfg, const msa_batch_t* ba
  * are the q_out rows t >= q_start[num_seqs] of a padded batch.  The sequences of
  * a call must not write to a common page, and k_new / v_new must not overlap
  * the caches, the scales or q_out.  A page id out of range, or a sequence of
- * more rows than max_q_per_seq, is recorded as MSA_ERR_DEVICE_BOUNDS and its
- * rows' cache writes are skipped.
+ * more rows than max_q_per_seq or its ctx_len, is recorded as
+ * MSA_ERR_DEVICE_BOUNDS and its rows' cache writes are skipped.
  */
 msa_status_t msa_qknorm_rope_insert_fp8(const msa_config_t* cfg, const msa_batch_t* batch, const void* q,
                                         const void* k_new, const void* v_new, const void* q_norm_w,

@@ -79,3 +79,18 @@ def test_a_nan_value_reaches_its_own_dim_only(cuda_ok, which):
     assert 0 < nan.sum() < nan.size // 16 and np.array_equal(np.isnan(got), nan)
     assert (np.abs(got - ref)[~nan] <= (2.0 ** -8 * np.abs(ref) + (2.0 ** -7 + 2.0 ** -12) * mag)[~nan]).all()
     assert np.abs(lse[:c.main].cpu().numpy() - ref_lse).max() <= T.LSE_ABS
+
+
+def test_insert_of_more_rows_than_the_context_holds_writes_nothing(cuda_ok):
+    """ctx_len 200 with 400 new rows: the positions would begin at -200.  Recorded, the caches stay, the other sequence's
+    rows are inserted."""
+    c = T._insert_case(73, ctx=[400, 130], nq=[400, 3], kv=2)
+    whole = T._insert(c)
+    c["batch"].ctx_len = torch.tensor([200, 130], dtype=torch.int32, device="cuda")
+    got = T._insert(c)
+    assert msa.device_status() == msa.MSA_ERR_DEVICE_BOUNDS
+    kept = c["table"][0][c["table"][0] >= 0]
+    other = c["table"][1][c["table"][1] >= 0]
+    for x, before, all_in in zip(got[1:], (*c["codes"], *c["scales"]), whole[1:]):
+        assert np.array_equal(x[torch.from_numpy(kept).long().cuda()].cpu().numpy(), before[kept])
+        assert torch.equal(x[torch.from_numpy(other).long().cuda()], all_in[torch.from_numpy(other).long().cuda()])
