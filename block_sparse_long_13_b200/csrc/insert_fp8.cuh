@@ -177,9 +177,10 @@ __device__ __forceinline__ void kv_insert_piece(const KvInsertArgs& a, const Rop
   const bool k_grown = slot0 == 0 || !k_held || kmax > E4M3_MAX * k_old;
   const bool v_grown = slot0 == 0 || !v_held || vmax > E4M3_MAX * v_old;
   const float ks = k_grown ? e4m3_block_scale(kmax) : k_old, vs = v_grown ? e4m3_block_scale(vmax) : v_old;
-  // a power of two's reciprocal is exact, and so is a product with it; other scales (a cache that something else wrote)
-  // are divided by
-  const bool exact = (((__float_as_uint(ks) | __float_as_uint(vs)) & 0x7FFFFFu) == 0u) && ks >= 0x1p-126f && vs >= 0x1p-126f;
+  // a power of two's reciprocal is exact, and so is a product with it; other scales (a cache that something else wrote),
+  // and 2^127, whose reciprocal is no normal number, are divided by
+  const bool exact = (((__float_as_uint(ks) | __float_as_uint(vs)) & 0x7FFFFFu) == 0u) && fminf(ks, vs) >= 0x1p-126f &&
+                     fmaxf(ks, vs) <= 0x1p126f;
   const float ki = __uint_as_float(0x7F000000u - __float_as_uint(ks)), vi = __uint_as_float(0x7F000000u - __float_as_uint(vs));
   uint8_t* kt = a.k_cache + tile * (128 * QKR_D);
   uint8_t* vt = a.v_cache + tile * (128 * QKR_D);

@@ -94,3 +94,17 @@ def test_insert_of_more_rows_than_the_context_holds_writes_nothing(cuda_ok):
     for x, before, all_in in zip(got[1:], (*c["codes"], *c["scales"]), whole[1:]):
         assert np.array_equal(x[torch.from_numpy(kept).long().cuda()].cpu().numpy(), before[kept])
         assert torch.equal(x[torch.from_numpy(other).long().cuda()], all_in[torch.from_numpy(other).long().cuda()])
+
+
+@pytest.mark.parametrize("power", [125, 126, 127])
+def test_insert_under_the_largest_scales(cuda_ok, power):
+    """A page that goes on under an old scale of 2^126 and more: a code is value / scale there too.  (Values of 2^120 need
+    no such scale, but the page keeps the one that it has.)"""
+    c = T._insert_case(74, ctx=[40, 77], nq=[4, 12], kv=1)
+    c["v_new"] = (c["v_new"].double().sign() * 2.0 ** torch.from_numpy(np.random.default_rng(0).uniform(118, 123, (16, 1, 128)))).to(torch.bfloat16)
+    for s in range(2):
+        c["scales"][1][c["table"][s, 0]] = 2.0 ** power
+    got = T._insert(c)
+    assert msa.device_status() == msa.MSA_OK
+    T._check_insert(c, got)
+    assert (got[2][int(c["table"][0, 0]), 0, 36:40] & 0x7F).any()
