@@ -58,7 +58,8 @@ class _CBatch(ctypes.Structure):
 
 _lib_handle = None
 # _bind.so, once the first of these calls is made: their checks and the call itself, natively.  A function of it answers None
-# for arguments that do not fit; the Python code behind each use then says what is wrong with them.
+# for arguments that do not fit; the Python code behind each use then says what is wrong with them, or, where _bind.so is
+# not there (_NotNative), makes the call.
 _calls = None
 _BOUND = ("msa_attn_decode_fp8", "msa_attn_prefill_fp8", "msa_qknorm_rope_insert_fp8", "msa_advance_batch")
 
@@ -113,18 +114,34 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     return lib
 
 
+class _NotNative:
+    """In the place of _bind.so: every call is left to Python."""
+    attn = insert = advance = staticmethod(lambda *_: None)
+
+
 def _native():
-    """_bind.so over the loaded library; raises if it is missing."""
+    """_bind.so over the loaded library; raises if it is missing or was built for another torch or Python."""
+    lib = load_library()
+    try:
+        from .build import bind_fits
+        if not bind_fits():
+            raise ImportError("_bind.so is missing or was built for another torch or Python")
+        from . import _bind
+    except ImportError as e:
+        raise RuntimeError("_bind.so is missing or does not fit this torch: build it with "
+                           "`python -m block_sparse_long_13_b200.build --force`") from e
+    _bind.setup(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in _BOUND))
+    return _bind
+
+
+def _first_call():
+    """What makes the calls over the 8-bit cache from now on."""
     global _calls
-    if _calls is None:
-        lib = load_library()
-        try:
-            from . import _bind
-        except ImportError as e:
-            raise RuntimeError("_bind.so is missing or does not fit this torch: build it with "
-                               "`python -m block_sparse_long_13_b200.build --force`") from e
-        _bind.setup(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in _BOUND))
-        _calls = _bind
+    load_library()                                   # raises if it is missing
+    try:
+        _calls = _native()
+    except RuntimeError:
+        _calls = _NotNative
     return _calls
 
 
@@ -353,7 +370,7 @@ def decode_fp8_workspace_bytes(cfg: Config, batch: Batch) -> int:
 
 
 def _attn_fp8(prefill, cfg, batch, q, k_cache, v_cache, k_scale, v_scale, block_idx, out, lse, workspace, stream):
-    status = (_calls or _native()).attn(prefill, cfg, batch, q, k_cache, v_cache, k_scale, v_scale, block_idx, out, lse,
+    status = (_calls or _first_call()).attn(prefill, cfg, batch, q, k_cache, v_cache, k_scale, v_scale, block_idx, out, lse,
                                         workspace, stream)
     if status is None:
         rows = (batch.total_q, cfg.num_q_heads)
@@ -388,7 +405,7 @@ def qknorm_rope_insert_fp8(cfg: Config, batch: Batch, q, k_new, v_new, q_norm_w,
                            eps: float = 1e-6, stream=None) -> None:
     """qknorm_rope_insert into an 8-bit cache (see include/msa.h): the queries go to q_out (q itself or another
     buffer), the new rows become codes, and the scales of their pages follow."""
-    status = (_calls or _native()).insert(cfg, batch, q, k_new, v_new, q_norm_w, k_norm_w, q_out, k_cache_e4m3,
+    status = (_calls or _first_call()).insert(cfg, batch, q, k_new, v_new, q_norm_w, k_norm_w, q_out, k_cache_e4m3,
                                           v_cache_e4m3, k_scale, v_scale, rotary_dim, rope_theta, eps, stream)
     if status is None:
         bf16, heads = torch.bfloat16, (batch.total_q, cfg.num_q_heads, cfg.head_dim)
@@ -410,7 +427,7 @@ def advance_batch(delta, ctx_len, page_table, free_ring, pool, ctx_len_out, pool
     given back to the ring, and ctx_len_out, q_start and page_table then serve as a Batch.  ctx_len_out may be ctx_len
     and pool_out may be pool.  All tensors int32; nothing is read back to the host: pool_out[2] says on the device how
     many pages the step lacked (0: done, -1: arguments that do not fit)."""
-    status = (_calls or _native()).advance(delta, ctx_len, page_table, free_ring, pool, ctx_len_out, pool_out, q_start,
+    status = (_calls or _first_call()).advance(delta, ctx_len, page_table, free_ring, pool, ctx_len_out, pool_out, q_start,
                                            slot_map, block_size, stream)
     if status is None:
         if page_table.dim() != 2:

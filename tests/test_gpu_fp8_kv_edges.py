@@ -108,3 +108,22 @@ def test_insert_under_the_largest_scales(cuda_ok, power):
     assert msa.device_status() == msa.MSA_OK
     T._check_insert(c, got)
     assert (got[2][int(c["table"][0, 0]), 0, 36:40] & 0x7F).any()
+
+
+def test_calls_without_the_native_module_give_the_same_bits(cuda_ok, monkeypatch):
+    """The checks of _bind.so and those of Python stand side by side: the same calls pass either."""
+    def results():
+        got = []
+        for which in T.FORMS:
+            c = T.Case(75, ctx=[300, 129], nq=[2, 1], which=which)
+            got += [*c.run(), c.run(lse=False)[0]]
+        got += T._insert(T._insert_case(76, ctx=[300, 129], nq=[20, 1], kv=2))
+        table, ring, pool = T._pool_case(9, [127, 300], [2, -45])
+        got += [torch.tensor(x) for x in T._advance([2, -45], [127, 300], table, ring, pool, 3)]
+        return got
+    native = results()
+    assert msa._calls is not msa._NotNative
+    monkeypatch.setattr(msa, "_calls", msa._NotNative)
+    for a, b in zip(native, results()):
+        assert torch.equal(a, b)
+    assert msa.device_status() == msa.MSA_OK
