@@ -909,6 +909,16 @@ bool few_slots(const msa_config_t* c, const msa_batch_t* b) {
   return slots + 5 * units <= std::min<int64_t>(24576, 8000 + 12 * buckets);
 }
 
+struct Span {
+  const void* at;
+  size_t bytes;
+  const char* what;
+};
+bool overlap(const Span& a, const Span& b) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+  return x < y + b.bytes && y < x + a.bytes;
+}
+
 // theta^(-2i/r) / (2 pi) turns of the rotation pairs, modulo 1, as multiples of 2^-64
 msa::RopeTable rope_table(int rotary_dim, float theta) {
   msa::RopeTable t{};
@@ -1054,6 +1064,21 @@ msa_status_t msa_qknorm_rope_insert_fp8(const msa_config_t* cfg, const msa_batch
   CHECK_SUP(static_cast<int64_t>(batch->num_seqs) + batch->total_q < (1LL << 31) / (cfg->num_kv_heads + 1),
             "too many sequences and rows");
   if (batch->total_q == 0) return MSA_OK;
+  {
+    // The queries' kernel runs beside the other one, and a page's codes are written by many threads: nothing that is written
+    // may lie over anything else, but for q_out in q's own place.
+    const size_t rows = static_cast<size_t>(batch->total_q) * 256, tiles = static_cast<size_t>(batch->num_pages) * cfg->num_kv_heads;
+    const size_t seqs = static_cast<size_t>(batch->num_seqs) * 4;
+    const Span all[] = {{q_out, rows * cfg->num_q_heads, "q_out"}, {k_cache_e4m3, tiles * 16384, "k_cache"},
+                        {v_cache_e4m3, tiles * 16384, "v_cache"}, {k_scale, tiles * 4, "k_scale"}, {v_scale, tiles * 4, "v_scale"},
+                        {q, rows * cfg->num_q_heads, "q"}, {k_new, rows * cfg->num_kv_heads, "k_new"},
+                        {v_new, rows * cfg->num_kv_heads, "v_new"}, {q_norm_w, 256, "q_norm_w"}, {k_norm_w, 256, "k_norm_w"},
+                        {batch->q_start, seqs + 4, "q_start"}, {batch->ctx_len, seqs, "ctx_len"},
+                        {batch->page_table, seqs * batch->max_blocks_per_seq, "page_table"}};
+    for (int w = 0; w < 5; ++w)                          // what is written
+      for (const Span& o : all)
+        CHECK_ARG(&o <= &all[w] || !overlap(all[w], o) || (w == 0 && &o == &all[5] && q_out == q), "%s and %s overlap", all[w].what, o.what);
+  }
   const msa::RopeTable tab = rope_table(rotary_dim, rope_theta);
   msa::KvInsertArgs a{};
   a.k_new = static_cast<const __nv_bfloat16*>(k_new);

@@ -315,8 +315,8 @@ msa_status_t msa_attn_prefill_fp8(const msa_config_t* cfg, const msa_batch_t* ba
  *   number counts as 0 (the page's earlier codes become 0).
  * Slots behind the last new row, and other pages, are left as they were, and so
  * are the q_out rows t >= q_start[num_seqs] of a padded batch.  The sequences of
- * a call must not write to a common page, and k_new / v_new must not overlap
- * the caches, the scales or q_out.  A page id out of range, or a sequence of
+ * a call must not write to a common page.  What is written must not overlap
+ * anything else, but for q_out = q (MSA_ERR_INVALID_ARG).  A page id out of range, or a sequence of
  * more rows than max_q_per_seq or its ctx_len, is recorded as
  * MSA_ERR_DEVICE_BOUNDS and its rows' cache writes are skipped.
  */
