@@ -10,10 +10,11 @@
 //   S^T = K_b Q^T   (M = 128 keys, N = 16 heads, K = 128 dims),   O_b^T = V_b^T P^T   (M = 128 dims, K = 128 keys),
 // which want Q and P in 8 bits too.  Neither is rounded to 8 bits: each is the sum of a few 8-bit numbers, which are
 // columns of one operand and whose products are added in fp32.
-//   Q is the sum of two e4m3 numbers, scaled per head by a power of two so that the largest |q| is in (224, 448].  A bf16 number has 8
-//      significant bits; the high part takes 4 of them, and the rest is a multiple of q's last bit by at most 8
-//      of them either way, which 4 bits hold: exact, down to elements 2^-11 below the head's largest (below it
-//      the error is 2^-10 of a scaled unit, at most 2^-17 of the largest element).
+//   Q is the sum of two e4m3 numbers, h + l / 16, scaled per head by a power of two so that the largest |q| is in (224, 448].
+//      A bf16 number has 8 significant bits; h takes 4 of them, and the rest is a multiple of q's last bit by at most 8 of
+//      them either way, which 4 bits hold: exact, down to elements 2^-14 of the head's largest, because the rest is at
+//      most 16 and the factor keeps it above e4m3's least step (below them off by 2^-14 of a scaled unit, 2^-21 of the largest
+//      element).  Without the factor elements below 2^-10 of it lost bits.
 //   P is the sum of three e5m2 numbers (3 significant bits each; the exponents of f16): 2^15 2^(x - m) <= 2^15, m the
 //      block's own maximum, as f16 h; then h = p1 + p2 / 8 + p3 / 64, each part the rest of those before it, rounded.  The rests
 //      are exact in f16, and the factors 8 and 64 keep them above e5m2's least number for as long as h is normal:
@@ -128,7 +129,7 @@ __device__ __forceinline__ float warp_max(float v) {
   return r;
 }
 
-// two values (<= 448) as high + low e4m3 pairs
+// two values (<= 448 in size) as e4m3 pairs, a = hi + lo / 16
 __device__ __forceinline__ void e4m3x2_split(float a, float b, uint32_t& hi, uint32_t& lo) {
   uint32_t h2, back, d;
   uint16_t u, v;
@@ -136,6 +137,7 @@ __device__ __forceinline__ void e4m3x2_split(float a, float b, uint32_t& hi, uin
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(u) : "r"(h2));
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(u));
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(h2), "r"(back));
+  asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(d) : "r"(0x4C004C00u));   // 16
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(v) : "r"(d));
   hi = u;
   lo = v;
@@ -514,7 +516,7 @@ attn_decode_fp8_kernel(const __grid_constant__ CUtensorMap tmap_k,    // k codes
           tmem_ld_wait();
           tc_fence_before();
 #pragma unroll
-          for (int h = 0; h < 16; ++h) x[h] = (v[h] + v[16 + h]) * (fq[h] * ks);
+          for (int h = 0; h < 16; ++h) x[h] = fmaf(v[16 + h], 0.0625f, v[h]) * (fq[h] * ks);
           if (row >= nvis) {                 // keys behind the query's position do not count
 #pragma unroll
             for (int h = 0; h < 16; ++h) x[h] = -INFINITY;

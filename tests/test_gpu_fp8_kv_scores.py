@@ -73,3 +73,16 @@ def test_a_row_is_as_exact_in_a_batch_as_alone(cuda_ok, which):
     out, lse = one.run()
     assert msa.device_status() == msa.MSA_OK
     one.check(out, lse, [0])
+
+
+@pytest.mark.parametrize("which", T.FORMS)
+def test_queries_with_one_large_element(cuda_ok, which):
+    """An element 2^10 times the others, which meets keys that are 0 there: the scores are the others' own, and their bits
+    count.  Those above 2^-14 of the largest (2^-4 here) are held exactly; the few below (one in 20) are off by up to 2^-22 of
+    it, 2^-12, which moves a score by about sqrt(128 / 20) * 2^-12 / sqrt(3) * 60 * 2^-6.5 / sqrt(128) = 2e-5."""
+    c = T.Case(63, ctx=[1, 2, 130, 900, 2100], nq=[1, 1, 2, 3, 1], which=which, kv=2, topk=6)
+    c.q[..., 3] = 1024.0
+    c.k[..., 3] = 0
+    out, lse = c.run()
+    assert msa.device_status() == msa.MSA_OK
+    c.check(out, lse, range(c.main))
