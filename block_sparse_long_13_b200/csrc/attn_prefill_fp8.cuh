@@ -723,9 +723,15 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
       // P at most 2^14: with V's 2^-15 that is 1/2, so that a sum of 128 codes of 448 stays an f16 number with room for the
       // rounding of m sc; -inf only on rows past the tile's entries
       const float mc = (m > -INFINITY) ? fmaf(m, sc, -14.f) : 0.f;
+      float off = mc;
+      if (fabsf(mc) >= 65536.f) {                 // huge scores: that rounding would be whole powers of two, so m goes first
+        off = -14.f;
+#pragma unroll
+        for (int c = 0; c < 32; ++c) { v0[c] -= m; v1[c] -= m; v2[c] -= m; v3[c] -= m; }
+      }
       // ---- P = exp2(scale * S - max) as f16 pairs into P[w] (TMEM), two halves of 64 keys
       float l0 = 0.f, l1 = 0.f;
-      const unsigned long long sc2 = pair(sc, sc), mc2 = pair(-mc, -mc);
+      const unsigned long long sc2 = pair(sc, sc), mc2 = pair(-off, -off);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         uint32_t pk[32];

@@ -86,3 +86,21 @@ def test_queries_with_one_large_element(cuda_ok, which):
     out, lse = c.run()
     assert msa.device_status() == msa.MSA_OK
     c.check(out, lse, range(c.main))
+
+
+@pytest.mark.parametrize("which", T.FORMS)
+@pytest.mark.parametrize("q_size", [3e6, 1e9, 1e20])
+def test_huge_scores(cuda_ok, which, q_size):
+    """Every key of a row the same, scores up to 2^86: equal probabilities, whatever the scores' last bits.  The output is
+    448 v_scale, moved by less than 2^-6 of itself (test_largest_values_under_equal_scores)."""
+    c = T.Case(64, ctx=[400, 257], nq=[3, 2], which=which)
+    c.k[:] = 0x7E
+    c.v[:] = 0x7E
+    c.ks[:] = 2.0 ** -6
+    c.vs[:] = 2.0 ** -7
+    c.q = torch.full_like(c.q, q_size)
+    out, lse = c.run()
+    assert msa.device_status() == msa.MSA_OK
+    assert ((out[:c.rows].float() - 3.5).abs() <= 3.5 * 2.0 ** -6).all(), (float(out.min()), float(out.max()))
+    want = float(c.q[0, 0, 0]) * 448 * 2.0 ** -6 * 128 ** 0.5
+    assert ((lse[:c.rows].double() - want).abs() <= 1e-5 * want).all()
