@@ -63,7 +63,7 @@ constexpr int ATD8_SMEM = ATD8_SLOTS * (2 * ATD8_TILE + ATD8_PT) + 2 * ATD8_QT +
 constexpr uint32_t ATD8_TM_S = 0, ATD8_TM_O = ATD8_SLOTS * 32, ATD8_TMEM = 512;   // 32 and 64 columns each: 16 a part
 constexpr int ATD8_PART = 16 * 128 + 32;   // floats of a partial result: sums [16][128], maxima [16], sums of p [16]
 constexpr float ATD8_PLOG = 15.f, ATD8_PINV = 0x1p-15f;   // a block's probabilities are held times 2^15
-constexpr float ATD8_LOW = -1e30f;     // start of the running maxima (finite: -inf - -inf is NaN)
+constexpr float ATD8_LOW = -3e38f;     // start of the running maxima (finite: -inf - -inf is NaN)
 
 struct AttnDecodeFp8Args {
   const __nv_bfloat16* q;        // [total_q][Hq][128]

@@ -829,7 +829,7 @@ __global__ void __launch_bounds__(256, 6) attn_merge_fp8_kernel(const MergeFp8Ar
     s_f[s][h] = v.y;
   }
   __syncthreads();
-  float mx = -1e30f;                        // finite: a row of NaN partials stays NaN
+  float mx = -3e38f;                        // finite: a row of NaN partials stays NaN
   for (int s = 0; s < a.topk; ++s) mx = fmaxf(mx, s_l[s][h]);
   float wsum = 0.f;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};

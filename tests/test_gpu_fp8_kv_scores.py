@@ -89,9 +89,9 @@ def test_queries_with_one_large_element(cuda_ok, which):
 
 
 @pytest.mark.parametrize("which", T.FORMS)
-@pytest.mark.parametrize("q_size", [3e6, 1e9, 1e20])
+@pytest.mark.parametrize("q_size", [3e6, 1e9, 1e20, -1e9, -1e30])
 def test_huge_scores(cuda_ok, which, q_size):
-    """Every key of a row the same, scores up to 2^86: equal probabilities, whatever the scores' last bits.  The output is
+    """Every key of a row the same, scores up to 2^86 and down to -2^106: equal probabilities, whatever the scores' last bits.  The output is
     448 v_scale, moved by less than 2^-6 of itself (test_largest_values_under_equal_scores)."""
     c = T.Case(64, ctx=[400, 257], nq=[3, 2], which=which)
     c.k[:] = 0x7E
@@ -103,4 +103,4 @@ def test_huge_scores(cuda_ok, which, q_size):
     assert msa.device_status() == msa.MSA_OK
     assert ((out[:c.rows].float() - 3.5).abs() <= 3.5 * 2.0 ** -6).all(), (float(out.min()), float(out.max()))
     want = float(c.q[0, 0, 0]) * 448 * 2.0 ** -6 * 128 ** 0.5
-    assert ((lse[:c.rows].double() - want).abs() <= 1e-5 * want).all()
+    assert ((lse[:c.rows].double() - want).abs() <= 1e-5 * abs(want)).all()
