@@ -685,7 +685,8 @@ attn_prefill_fp8_kernel(const __grid_constant__ CUtensorMap tmap_q,     // q as 
     for (int j = 0; j < nj && ok; ++j) {         // exit decisions are uniform over the warp
       const int nbucket = h0.x, n = h1.y & 15;
       const float ks = __int_as_float(h1.z), vs = __int_as_float(h1.w);
-      const float sc = fmaxf(a.scale_log2 * fabsf(ks), 1e-36f);   // not 0: the masked -inf * 0 is NaN
+      const float sa = a.scale_log2 * fabsf(ks);
+      const float sc = sa < 1e-36f ? 1e-36f : sa;   // not 0: the masked -inf * 0 is NaN; a NaN scale stays NaN
       const bool valid = e < n;
       const int t = ent >> 6;
       const long part = (static_cast<long>(t) * a.Hkv + h0.z) * a.topk + (ent & 63);

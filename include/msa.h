@@ -275,7 +275,8 @@ msa_status_t msa_merge_partials(int32_t n, int64_t units, int32_t head_dim, cons
  *   k_cache_e4m3  uint8 [num_pages][num_kv_heads][block_size][head_dim]   (v_cache_e4m3 alike)
  *   k_scale       fp32  [num_pages][num_kv_heads]                         (v_scale alike)
  *   key value = code * k_scale[page][g]
- * Any finite scale is read; msa_qknorm_rope_insert_fp8 writes powers of two.
+ * Any finite scale is read, and a NaN one makes its block's keys or values NaN;
+ * msa_qknorm_rope_insert_fp8 writes powers of two.
  * Unlike the bf16 caches, slots past a sequence's ctx_len may hold any bytes.
  *
  * msa_attn_decode_fp8 / msa_attn_prefill_fp8: the results of msa_attn_decode /

@@ -127,3 +127,15 @@ def test_calls_without_the_native_module_give_the_same_bits(cuda_ok, monkeypatch
     for a, b in zip(native, results()):
         assert torch.equal(a, b)
     assert msa.device_status() == msa.MSA_OK
+
+
+@pytest.mark.parametrize("which", T.FORMS)
+def test_a_nan_scale_makes_its_block_nan(cuda_ok, which):
+    c = T.Case(77, ctx=[300, 300, 300], nq=[2, 2, 2], which=which, kv=2, topk=3)
+    c.ks[c.table[0, 1], 1] = float("nan")
+    c.vs[c.table[1, 0], 0] = float("nan")
+    out, lse = c.run()
+    assert msa.device_status() == msa.MSA_OK
+    assert out[0:2, 16:].isnan().all() and lse[0:2, 16:].isnan().all() and not out[0:2, :16].isnan().any()
+    assert out[2:4, :16].isnan().all() and not lse[2:4].isnan().any() and not out[2:4, 16:].isnan().any()
+    c.check(out, lse, [4, 5])
