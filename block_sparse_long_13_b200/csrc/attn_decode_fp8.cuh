@@ -38,13 +38,14 @@
 // 1 the MMAs of S^T, 2 those of O^T; 4-7 and 12-15 run the softmax on alternate blocks (thread = key; each group keeps
 // the running maxima M of its own blocks of the row), 8-11
 // keep the output of either group's blocks (thread = dim): acc = acc 2^(M_old - M) + vs_b 2^(m - M) O_b.  The chain of a block's
-// softmax is longer than the 0.74 us that its 32 KiB take at the copy bandwidth: hence two groups.  An MMA as
+// softmax is longer than the 0.74 us that its 32 KiB take at the copy bandwidth (less where rows share blocks): hence two groups.  An MMA as
 // narrow as these takes 47 clocks whatever its N (measured, N <= 64), so the parts are the 16-wide pieces of
 // one operand (N = 32 and 48), and the pieces of the result are added when it is read.  Every wait is bounded.
-// Measured: 64 rows over 128K keys, 16 blocks, 4 groups: 29.1 us with the merge (134 MB of codes: 4.6 TB/s), of which 21 us
-// are the stream and 8 set-up, first look-ups, first pass through the code and merge; one row over 32K 10.3 us; 32 x 4
-// verify rows 51.7 us.  Three parts of P instead of two, and the factor 2^(m - M), cost 1.1 and 2.7 us of that, half of it in the
-// softmax and half in the output warps; parts by truncation, or a factor for distant blocks only, changed nothing.
+// Measured: 64 rows over 128K keys, 16 blocks, 4 groups: 29.1 to 31.0 us with the merge on two GPUs (134 MB of codes, of which
+// rows share some: 116 MB); a block takes 0.66 to 0.74 us a CTA (16 more blocks a row: +20.4 us, 32 more: +36.7), and 10.7 us are
+// set-up, first look-ups, first pass through the code and merge; one row over 32K 9.8 to 10.3 us; 32 x 4 verify rows 51.7 to 53.1 us.  Three parts of P instead of two, and the factor
+// 2^(m - M), cost 0.6 to 1.1 and 2.4 to 2.7 us of that, half of it in the softmax and half in the output warps; parts by
+// truncation, or a factor for distant blocks only, changed nothing.
 #pragma once
 #include "attn_decode.cuh"
 #include "e4m3.cuh"

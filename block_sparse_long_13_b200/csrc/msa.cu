@@ -899,10 +899,10 @@ msa_status_t run_decode_fp8(const msa_config_t* cfg, const msa_batch_t* batch, c
 // Which form a prefill call takes.  The slots take about 9.5 us + 3.7 ns a slot + 11 ns a (row, group), the tiles 24 us +
 // 2.2 ns a slot + 3.5 ns a (row, group) + 17 ns a bucket (its codes are widened, its last tile is not full); the page table's
 // width stands for the buckets of a sequence, so a cap keeps a table much wider than the contexts from deciding.  Measured,
-// us, slots / tiles, 16 blocks a row and 4 groups: 64 rows of a 32K context 27 / 46, 192 rows 63 / 67, 256 rows 81 / 75, 512
-// rows 151 / 111; 64 rows of a 4K context 27 / 37, 128 rows 45 / 48, 256 rows 81 / 64; 8 x 32 rows of 8K contexts 78 / 117; 4
-// blocks a row, one group: 512 rows 22 / 33, 1024 rows 35 / 35, 2048 rows 63 / 45; one block a row, one group: 1024 rows 21 /
-// 29, 2048 rows 36 / 33.
+// us, slots / tiles, 16 blocks a row and 4 groups: 64 rows of a 32K context 28 / 47, 192 rows 69 / 67, 256 rows 88 / 78, 512
+// rows 168 / 114; 64 rows of a 4K context 28 / 40, 128 rows 48 / 48, 256 rows 88 / 70; 8 x 32 rows of 8K contexts 87 / 112; 4
+// blocks a row, one group: 512 rows 22 / 29, 1024 rows 38 / 37, 2048 rows 70 / 49; one block a row, one group: 1024 rows 22 /
+// 27, 2048 rows 38 / 31.  (At the border the form taken is within 3 % of the other.)
 bool few_slots(const msa_config_t* c, const msa_batch_t* b) {
   const int64_t units = static_cast<int64_t>(b->total_q) * c->num_kv_heads, slots = units * c->topk;
   const int64_t buckets = std::min(slots, static_cast<int64_t>(b->num_seqs) * c->num_kv_heads * b->max_blocks_per_seq);
