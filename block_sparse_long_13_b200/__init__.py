@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
@@ -140,7 +141,8 @@ def _first_call():
     load_library()                                   # raises if it is missing
     try:
         _calls = _native()
-    except RuntimeError:
+    except RuntimeError as e:
+        warnings.warn(f"{e}; until then the calls over the 8-bit cache go through ctypes, some microseconds slower")
         _calls = _NotNative
     return _calls
 

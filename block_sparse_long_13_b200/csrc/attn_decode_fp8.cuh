@@ -21,8 +21,8 @@
 //      off by 2^-11 of itself (f16's 2^-12 included: 2^-10.4) down to probabilities of 2^-29 of the block's largest, by 2^-38
 //      of the block's largest below.  A row may put nearly all its weight on one key whose value is near 0 (a sink): its
 //      output is then made of the small ones, so what counts is their own size, not the largest one's.  Two e4m3 parts under
-//      the row's running maximum, which end at 2^-18 of it, lost a quarter of such an output 12 nats below the sink and all of it from 13.
-//      The sum of probabilities is taken from the unrounded fp32 values.
+//      the row's running maximum, which end at 2^-18 of it, lost a quarter of such an output 12 nats below the sink and all
+//      of it from 13.  The sum of probabilities is taken from the unrounded fp32 values.
 // Converting the tiles to 16 bits in shared memory instead would read and write 96 KiB of it a block and
 // keep a warpgroup busy.
 //
@@ -36,16 +36,15 @@
 // one barrier a block (a wait for a barrier that is ready takes about 100 clocks, measured, and a block has 1,400).
 // Warps: 3 looks up slots (32 at a time: block id, sequence, page, scales) and splits the queries, 0 issues the copies,
 // 1 the MMAs of S^T, 2 those of O^T; 4-7 and 12-15 run the softmax on alternate blocks (thread = key; each group keeps
-// the running maxima M of its own blocks of the row), 8-11
-// keep the output of either group's blocks (thread = dim): acc = acc 2^(M_old - M) + vs_b 2^(m - M) O_b.  The chain of a block's
-// softmax is longer than the 0.74 us that its 32 KiB take at the copy bandwidth (less where rows share blocks): hence two groups.  An MMA as
-// narrow as these takes 47 clocks whatever its N (measured, N <= 64), so the parts are the 16-wide pieces of
+// the running maxima M of its own blocks of the row), 8-11 keep the output of either group's blocks (thread = dim):
+// acc = acc 2^(M_old - M) + vs_b 2^(m - M) O_b.  The chain of a block's softmax is longer than the 0.74 us that its 32 KiB
+// take at the copy bandwidth (less where rows share blocks): hence two groups.  An MMA as narrow as these takes 47 clocks whatever its N (measured, N <= 64), so the parts are the 16-wide pieces of
 // one operand (N = 32 and 48), and the pieces of the result are added when it is read.  Every wait is bounded.
 // Measured: 64 rows over 128K keys, 16 blocks, 4 groups: 29.1 to 31.0 us with the merge on two GPUs (134 MB of codes, of which
-// rows share some: 116 MB); a block takes 0.66 to 0.74 us a CTA (16 more blocks a row: +20.4 us, 32 more: +36.7), and 10.7 us are
-// set-up, first look-ups, first pass through the code and merge; one row over 32K 9.8 to 10.3 us; 32 x 4 verify rows 51.7 to 53.1 us.  Three parts of P instead of two, and the factor
-// 2^(m - M), cost 0.6 to 1.1 and 2.4 to 2.7 us of that, half of it in the softmax and half in the output warps; parts by
-// truncation, or a factor for distant blocks only, changed nothing.
+// rows share some: 116 MB); a block takes 0.66 to 0.74 us a CTA (16 more blocks a row: +20.4 us, 32 more: +36.7), and 10.7 us
+// are set-up, first look-ups, first pass through the code and merge; one row over 32K 9.8 to 10.3 us; 32 x 4 verify rows 51.7
+// to 53.1 us.  Three parts of P instead of two, and the factor 2^(m - M), cost 0.6 to 1.1 and 2.4 to 2.7 us of that, half of it
+// in the softmax and half in the output warps; parts by truncation, or a factor for distant blocks only, changed nothing.
 #pragma once
 #include "attn_decode.cuh"
 #include "e4m3.cuh"

@@ -22,7 +22,7 @@
 // partials go straight from the registers to memory instead of by way of shared memory (230 -> 221 and 2.42 ms alike; that
 // alone, with one buffer: 235 and 2.58).  V's factor and the rare forms (NaN codes, huge scores) cost 221 -> 228.  P handed over
 // in halves changed nothing.  The last 16,384 rows of 128K take 2.4
-// ms: schedule 0.04, tiles 1.64 (650 TFLOP/s of S and P V), merge 0.68 at 6.4 TB/s.
+// ms: schedule 0.04, tiles 1.64 (670 TFLOP/s of S and P V), merge 0.68 at 6.4 TB/s.
 #pragma once
 #include "attn_prefill.cuh"
 #include "e4m3.cuh"
